@@ -74,6 +74,16 @@ enum { NVFP4_RNE = 0, NVFP4_SR = 1 };            /* rounding of element codes */
 enum { NVFP4_SCALE_1D = 0, NVFP4_SCALE_2D = 1 };  /* 16 along K | 16x16 tile */
 enum { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 };   /* GEMM / dequantize output type */
 
+/* Activations of the linear layer's epilogue. */
+enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_RELU = 1,
+    NVFP4_ACT_RELU2 = 2,       /* max(z, 0)^2 */
+    NVFP4_ACT_GELU = 3,        /* z P(z), P the normal distribution function */
+    NVFP4_ACT_GELU_TANH = 4,   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    NVFP4_ACT_SILU = 5         /* z / (1 + exp(-z)) */
+};
+
 /* Library ABI version (major * 100 + minor): 101 = 1.1, the 1.0 entry points
  * plus the dual, from-amax, GEMM-amax, MXFP4 and RHT-order ones. */
 int nvfp4_version(void);
@@ -279,6 +289,8 @@ nvfp4_status nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int s
  *   Shapes: M, N >= 1; K a multiple of 64 (K/2 bytes per code row, 16-byte
  *   aligned); ragged M and N tails are handled.  c 16-byte aligned and ldc a
  *   multiple of 8 elements.
+ *   With an N that is no multiple of 16 bytes of C, the columns from N to the
+ *   end of that 16-byte unit are written as zeros (they lie inside ldc).
  *   Kernel: pairs of CTAs on two SMs computing 256 x 256 tiles (tcgen05
  *   cta_group::2); the environment variable NVFP4_GEMM_PAIR=0 selects the
  *   single-SM kernel (128 x 256 tiles), which meets the same tolerance. */
@@ -337,6 +349,132 @@ nvfp4_status nvfp4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
 nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mma, const uint8_t* b_codes,
                               const uint8_t* b_scales_mma, int64_t M, int64_t N, int64_t K, int out_dtype, void* c,
                               int64_t ldc, void* stream);
+
+/* ------------------------------------------------------- the linear layer --
+ * The product with what a layer puts around it, and its gradient ["Presisi
+ * sebagai tombol throughput" -- most step time is in the matmuls, so what
+ * follows them belongs into their epilogue; "NVFP4 Is a Scaling System",
+ * "Where speed and accuracy claims can fail" -- work around the matmuls
+ * counts].
+ *
+ * nvfp4_gemm_epilogue:
+ *   z = alpha A . B^T + bias,   C = act(z) + residual
+ *   Operands, shapes, alpha, C and alignment as nvfp4_gemm; M from 1.
+ *   bias       bf16 [N] (2-byte aligned), nullable.
+ *   activation one of NVFP4_ACT_*.
+ *   residual   bf16 [M x ldr], nullable; ldr >= N a multiple of 8, 16-byte
+ *              aligned.  It may be C itself (bf16 C, ldr == ldc).
+ *   pre        bf16 [M x ldp], nullable: receives RN(z), what the gradient
+ *              needs; ldp and alignment as residual.
+ *   c_amax     as nvfp4_gemm_amax, nullable.
+ *   All of it is binary32; z is rounded only where it is stored, C once.
+ *   Columns from N on are left as they were, in C and in pre. */
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                 const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs, int64_t M,
+                                 int64_t N, int64_t K, const void* bias, int activation, const void* residual,
+                                 int64_t ldr, int out_dtype, void* c, int64_t ldc, void* pre, int64_t ldp,
+                                 float* c_amax, void* stream);
+
+/* The epilogue's gradient: dz = RN(dy * act'(z)), dbias = column sums of
+ * dy * act'(z) (binary32, in a fixed order), amax = max |dz| as stored, ready
+ * for nvfp4_quantize_1d_from_amax.  (The residual's gradient is dy itself, the
+ * operands' are the dgrad and wgrad products of dz.)
+ *   dy [M x ldy], z [M x ldz] (as `pre` above; not read, may be NULL, for
+ *   NVFP4_ACT_NONE), dz [M x lddz]: bf16, strides multiples of 8 and >= N,
+ *   16-byte aligned.  dz may be dy or z itself (same stride).
+ *   experts = 0: M rows, dbias [N].  experts > 0: rows sorted by expert as
+ *   nvfp4_moe_sort's offsets and counts say (M their number of rows, a
+ *   multiple of 128), dbias [experts x N]; rows without a token become zeros
+ *   in dz and count nowhere.
+ *   dbias, amax nullable.  Workspace, with dbias: >=
+ *   nvfp4_act_grad_workspace_size(M, N) bytes, 16-byte aligned. */
+size_t nvfp4_act_grad_workspace_size(int64_t M, int64_t N);
+nvfp4_status nvfp4_act_grad(const void* dy, int64_t ldy, const void* z, int64_t ldz, int64_t M, int64_t N,
+                            int activation, const int32_t* offsets, const int32_t* counts, int64_t experts, void* dz,
+                            int64_t lddz, float* dbias, float* amax, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* ---------------------------------------------------- the layer of experts --
+ * A linear layer with one weight per expert over tokens that were routed to
+ * topk experts each.  The copies of the tokens are sorted by expert into
+ * segments of rows that start at multiples of 128 (one chunk of the MMA scale
+ * layout, so that a quantizer's output for the sorted rows is the segments'
+ * operands as it is); rows of a segment behind its last copy, and rows behind
+ * the last segment, are padding: every call below writes zeros there.
+ *
+ * nvfp4_moe_sort: stable sort of `copies` = tokens x topk expert numbers.
+ *   expert_ids int32 [copies], copy c = token c / topk; a number outside
+ *              [0, experts) drops the copy.
+ *   rows       rows of the sorted matrices, a multiple of 128.
+ *              nvfp4_moe_rows(copies, experts) suffice for every routing; with
+ *              fewer, copies that find no row are dropped.
+ *   offsets    int32 [experts + 1]: first row of each segment (the last entry:
+ *              end of the last one), multiples of 128.
+ *   counts     int32 [experts]: copies in each segment.
+ *   row_copy   int32 [rows]: the row's copy, -1 for padding.
+ *   copy_row   int32 [copies]: the copy's row, -1 if dropped.
+ *   Workspace: >= nvfp4_moe_workspace_size(copies, experts), 16-byte aligned.
+ *   experts in [1, 1024].
+ * The calls below take these arrays as device data; values that no sort would
+ * give are not followed out of bounds, but the results are then unspecified. */
+int64_t nvfp4_moe_rows(int64_t copies, int64_t experts);
+size_t nvfp4_moe_workspace_size(int64_t copies, int64_t experts);
+nvfp4_status nvfp4_moe_sort(const int32_t* expert_ids, int64_t copies, int64_t experts, int64_t rows,
+                            int32_t* offsets, int32_t* counts, int32_t* row_copy, int32_t* copy_row, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* y[copy_row[t topk + j]] = x[t], padding rows 0; amax (nullable) = max |x| of
+ * the tokens that were sent anywhere, i.e. of y.  x bf16 [tokens x ldx], y
+ * bf16 [rows x ldy], cols and the strides multiples of 8, 16-byte aligned.
+ * Its gradient is nvfp4_moe_combine without weights. */
+nvfp4_status nvfp4_moe_gather(const void* x, int64_t ldx, int64_t tokens, int64_t topk, int64_t cols,
+                              const int32_t* copy_row, const int32_t* row_copy, int64_t rows, void* y, int64_t ldy,
+                              float* amax, void* stream);
+
+/* out[t] = RN(residual[t] + sum_j weights[t][j] y[copy_row[t topk + j]]), the
+ * sum in binary32 in the order of j, dropped copies left out.  weights binary32
+ * [tokens x topk], nullable (all 1); residual bf16 [tokens x ldr], nullable,
+ * may be out itself (same stride); y bf16 [rows x ldy], out bf16 [tokens x
+ * ldo], cols and strides as nvfp4_moe_gather. */
+nvfp4_status nvfp4_moe_combine(const void* y, int64_t ldy, int64_t rows, int64_t cols, const int32_t* copy_row,
+                               const float* weights, const void* residual, int64_t ldr, int64_t tokens, int64_t topk,
+                               void* out, int64_t ldo, void* stream);
+
+/* The gradient of nvfp4_moe_combine: dy[row] = RN(weight dout[t]) for each
+ * copy's row, padding rows 0; dweights[t][j] = <dout[t], y[row]> in binary32
+ * in a fixed order, 0 for dropped copies; amax (nullable) = max |dy|.
+ * weights nullable (all 1); dweights nullable, y is then not read. */
+nvfp4_status nvfp4_moe_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t ldy, int64_t tokens,
+                                    int64_t topk, int64_t cols, const int32_t* copy_row, const int32_t* row_copy,
+                                    int64_t rows, const float* weights, void* dy, int64_t lddy, float* dweights,
+                                    float* amax, void* stream);
+
+/* The experts' products: nvfp4_gemm_epilogue over sorted rows, rows of expert e
+ * with weight e.  A [M rows] as quantized from sorted rows (M a multiple of
+ * 128); b_codes [experts x N x K/2], b_scales_mma experts x
+ * nvfp4_mma_scale_bytes(N, K) bytes, b_gs [experts]; bias [experts x N].
+ * Padding rows of C and pre become zeros (the residual is not added there),
+ * whatever A holds in them.  With the codes of the transposed weights this is
+ * the gradient with respect to A. */
+nvfp4_status nvfp4_gemm_grouped(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs,
+                                const int32_t* offsets, const int32_t* counts, int64_t experts, int64_t M, int64_t N,
+                                int64_t K, const void* bias, int activation, const void* residual, int64_t ldr,
+                                int out_dtype, void* c, int64_t ldc, void* pre, int64_t ldp, float* c_amax,
+                                void* stream);
+
+/* The experts' weight gradients: C_e = alpha sum_k a[:, k] b[:, k]^T over the
+ * sorted rows k of expert e, c [experts x M x ldc] FP32 or bf16; the matrix of
+ * an expert without rows becomes zeros.  a [M x K] and b [N x K] are the
+ * transposed operands quantized over all K sorted rows (nvfp4_quantize_1d /
+ * nvfp4_rht_quantize_sr with transpose = 1; K a multiple of 128): blocks of 16
+ * and Hadamard chunks of up to 64 rows do not cross segments.  K is summed up
+ * to the end of the 64-row group that holds the segment's last copy; the rows
+ * behind it must be zeros, which gather and the products leave there. */
+nvfp4_status nvfp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                      const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs,
+                                      const int32_t* offsets, const int32_t* counts, int64_t experts, int64_t M,
+                                      int64_t N, int64_t K, int out_dtype, void* c, int64_t ldc, void* stream);
 
 /* Number of kernels (and memset nodes excluded) this library has enqueued in
  * this process; instrumentation for benchmarks. */

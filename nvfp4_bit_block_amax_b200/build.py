@@ -26,9 +26,10 @@ UNITS = {
     "quant.cu": ["--fmad=false"],
     "gemm.cu": [],
     "mxfp4.cu": [],
+    "layer.cu": [],
     "api.cu": [],
 }
-HEADERS = ["common.cuh", "internal.h"]
+HEADERS = ["activation.cuh", "common.cuh", "internal.h", "tc.cuh"]
 
 
 def _nvcc() -> str:

@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/nvfp4.h"
+#include "activation.cuh"
 #include "internal.h"
 
 using namespace nvfp4;
@@ -12,8 +13,19 @@ namespace {
 
 std::atomic<long long> g_launches{0};
 
+static_assert((int)NVFP4_ACT_NONE == ACT_NONE && (int)NVFP4_ACT_RELU == ACT_RELU && (int)NVFP4_ACT_RELU2 == ACT_RELU2 &&
+                  (int)NVFP4_ACT_GELU == ACT_GELU && (int)NVFP4_ACT_GELU_TANH == ACT_GELU_TANH &&
+                  (int)NVFP4_ACT_SILU == ACT_SILU,
+              "the kernels' activations are the header's");
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+// A bf16 matrix: row stride of whole 16-byte units that holds `cols`, base on a 16-byte boundary.
+nvfp4_status check_bf16_matrix(const void* p, int64_t ld, int64_t cols) {
+    if (!p || ld < cols) return NVFP4_ERR_INVALID_ARG;
+    return ld % 8 || !aligned16(p) ? NVFP4_ERR_MISALIGNED : NVFP4_OK;
+}
 
 constexpr size_t kWorkspaceBytes = (size_t)kMaxPartials * sizeof(uint32_t);
 constexpr int64_t kMaxDim = (int64_t)1 << 31;   // TMA and index arithmetic bound per dimension
@@ -356,6 +368,280 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
                               int64_t ldc, void* stream) {
     return gemm_impl(a_codes, a_scales_mma, nullptr, b_codes, b_scales_mma, nullptr, M, N, K, out_dtype, c, ldc,
                      nullptr, stream, 1);
+}
+
+static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
+    if (!g.a || !g.sfa || !g.a_gs || !g.b || !g.sfb || !g.b_gs || !g.c) return NVFP4_ERR_INVALID_ARG;
+    if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_INVALID_ARG;
+    if (g.act < 0 || g.act >= kNumActivations) return NVFP4_ERR_INVALID_ARG;
+    if (g.M < 1 || g.N < 1 || g.K < 1 || g.ldc < g.N || g.M >= kMaxDim || g.N >= kMaxDim || g.K >= kMaxDim)
+        return NVFP4_ERR_INVALID_ARG;
+    if ((g.residual && g.ldr < g.N) || (g.pre && g.ldp < g.N)) return NVFP4_ERR_INVALID_ARG;
+    if (g.experts && (!g.offsets || !g.counts || g.experts < 1 || g.experts > kMaxExpertsArg ||
+                      g.experts * g.N >= kMaxDim || g.experts * g.M >= kMaxDim * 128))
+        return NVFP4_ERR_INVALID_ARG;
+    if (g.K % 64 || (g.experts && (g.wgrad ? g.K : g.M) % 128)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(g.a) || !aligned16(g.b) || !aligned16(g.sfa) || !aligned16(g.sfb) || !aligned16(g.c) || g.ldc % 8 ||
+        !aligned4(g.a_gs) || !aligned4(g.b_gs) || !aligned2(g.bias) || !aligned4(g.c_amax) || !aligned4(g.offsets) ||
+        !aligned4(g.counts) || (g.residual && (!aligned16(g.residual) || g.ldr % 8)) ||
+        (g.pre && (!aligned16(g.pre) || g.ldp % 8)))
+        return NVFP4_ERR_MISALIGNED;
+    g.out_bf16 = out_dtype == NVFP4_OUT_BF16;
+    if (g.c_amax &&
+        cudaMemsetAsync(g.c_amax, 0, sizeof(float), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+    cudaError_t e = launch_gemm_ext(g, static_cast<cudaStream_t>(stream));
+    g_launches += 1;
+    return from_cuda(e);
+}
+
+static GemmExtArgs operands(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                            const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs, int64_t M,
+                            int64_t N, int64_t K, void* c, int64_t ldc) {
+    GemmExtArgs g{};
+    g.a = a_codes;
+    g.sfa = a_scales_mma;
+    g.a_gs = a_gs;
+    g.b = b_codes;
+    g.sfb = b_scales_mma;
+    g.b_gs = b_gs;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.c = c;
+    g.ldc = ldc;
+    return g;
+}
+
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                 const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs, int64_t M,
+                                 int64_t N, int64_t K, const void* bias, int activation, const void* residual,
+                                 int64_t ldr, int out_dtype, void* c, int64_t ldc, void* pre, int64_t ldp,
+                                 float* c_amax, void* stream) {
+    GemmExtArgs g = operands(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, c, ldc);
+    g.bias = bias;
+    g.act = activation;
+    g.residual = residual;
+    g.ldr = ldr;
+    g.pre = pre;
+    g.ldp = ldp;
+    g.c_amax = c_amax;
+    return gemm_ext(g, out_dtype, stream);
+}
+
+nvfp4_status nvfp4_gemm_grouped(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs,
+                                const int32_t* offsets, const int32_t* counts, int64_t experts, int64_t M, int64_t N,
+                                int64_t K, const void* bias, int activation, const void* residual, int64_t ldr,
+                                int out_dtype, void* c, int64_t ldc, void* pre, int64_t ldp, float* c_amax,
+                                void* stream) {
+    if (experts < 1) return NVFP4_ERR_INVALID_ARG;
+    GemmExtArgs g = operands(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, c, ldc);
+    g.offsets = offsets;
+    g.counts = counts;
+    g.experts = experts;
+    g.bias = bias;
+    g.act = activation;
+    g.residual = residual;
+    g.ldr = ldr;
+    g.pre = pre;
+    g.ldp = ldp;
+    g.c_amax = c_amax;
+    return gemm_ext(g, out_dtype, stream);
+}
+
+nvfp4_status nvfp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
+                                      const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs,
+                                      const int32_t* offsets, const int32_t* counts, int64_t experts, int64_t M,
+                                      int64_t N, int64_t K, int out_dtype, void* c, int64_t ldc, void* stream) {
+    if (experts < 1) return NVFP4_ERR_INVALID_ARG;
+    GemmExtArgs g = operands(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, c, ldc);
+    g.offsets = offsets;
+    g.counts = counts;
+    g.experts = experts;
+    g.wgrad = 1;
+    return gemm_ext(g, out_dtype, stream);
+}
+
+size_t nvfp4_act_grad_workspace_size(int64_t M, int64_t N) {
+    return M < 1 || N < 1 ? 0 : (size_t)(ceil_div(M, 128) * N) * sizeof(float);
+}
+
+nvfp4_status nvfp4_act_grad(const void* dy, int64_t ldy, const void* z, int64_t ldz, int64_t M, int64_t N,
+                            int activation, const int32_t* offsets, const int32_t* counts, int64_t experts, void* dz,
+                            int64_t lddz, float* dbias, float* amax, void* workspace, size_t ws_bytes,
+                            void* stream) {
+    if (activation < 0 || activation >= kNumActivations) return NVFP4_ERR_INVALID_ARG;
+    if (M < 1 || N < 1 || M >= kMaxDim || N >= kMaxDim || ceil_div(M, 128) * ceil_div(N, 256) >= kMaxDim)
+        return NVFP4_ERR_INVALID_ARG;
+    if (experts < 0 || experts > kMaxExpertsArg || (experts && (!offsets || !counts))) return NVFP4_ERR_INVALID_ARG;
+    if (experts && M % 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    nvfp4_status st = check_bf16_matrix(dy, ldy, N);
+    if (st == NVFP4_OK) st = check_bf16_matrix(dz, lddz, N);
+    if (st == NVFP4_OK && activation != NVFP4_ACT_NONE) st = check_bf16_matrix(z, ldz, N);
+    if (st != NVFP4_OK) return st;
+    if (!aligned4(dbias) || !aligned4(amax) || (experts && (!aligned4(offsets) || !aligned4(counts))))
+        return NVFP4_ERR_MISALIGNED;
+    if (dbias && (!workspace || ws_bytes < nvfp4_act_grad_workspace_size(M, N) || !aligned16(workspace)))
+        return NVFP4_ERR_WORKSPACE;
+    ActGradArgs a{};
+    a.dy = dy;
+    a.ldy = ldy;
+    a.z = z;
+    a.ldz = ldz;
+    a.M = M;
+    a.N = N;
+    a.act = activation;
+    a.offsets = experts ? offsets : nullptr;
+    a.counts = counts;
+    a.experts = experts;
+    a.dz = dz;
+    a.lddz = lddz;
+    a.dbias = dbias;
+    a.amax = amax;
+    a.workspace = static_cast<float*>(workspace);
+    int n = 0;
+    cudaError_t e = launch_act_grad(a, static_cast<cudaStream_t>(stream), &n);
+    g_launches += n;
+    return from_cuda(e);
+}
+
+int64_t nvfp4_moe_rows(int64_t copies, int64_t experts) {
+    if (copies < 1 || experts < 1 || copies >= kMaxDim || experts > kMaxExpertsArg) return 0;
+    return ceil_div(copies + 127 * (copies < experts ? copies : experts), 128) * 128;
+}
+
+size_t nvfp4_moe_workspace_size(int64_t copies, int64_t experts) {
+    if (copies < 1 || experts < 1 || copies >= kMaxDim || experts > kMaxExpertsArg) return 0;
+    return moe_sort_workspace(copies, experts);
+}
+
+nvfp4_status nvfp4_moe_sort(const int32_t* expert_ids, int64_t copies, int64_t experts, int64_t rows,
+                            int32_t* offsets, int32_t* counts, int32_t* row_copy, int32_t* copy_row, void* workspace,
+                            size_t ws_bytes, void* stream) {
+    if (!expert_ids || !offsets || !counts || !row_copy || !copy_row) return NVFP4_ERR_INVALID_ARG;
+    if (copies < 1 || experts < 1 || rows < 1 || experts > kMaxExpertsArg || copies >= kMaxDim || rows >= kMaxDim ||
+        nvfp4_moe_rows(copies, experts) >= kMaxDim)
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows % 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned4(expert_ids) || !aligned4(offsets) || !aligned4(counts) || !aligned4(row_copy) || !aligned4(copy_row))
+        return NVFP4_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < moe_sort_workspace(copies, experts) || !aligned16(workspace))
+        return NVFP4_ERR_WORKSPACE;
+    SortArgs a{};
+    a.ids = expert_ids;
+    a.n = copies;
+    a.experts = experts;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.counts = counts;
+    a.row_copy = row_copy;
+    a.copy_row = copy_row;
+    a.workspace = static_cast<int32_t*>(workspace);
+    int n = 0;
+    cudaError_t e = launch_moe_sort(a, static_cast<cudaStream_t>(stream), &n);
+    g_launches += n;
+    return from_cuda(e);
+}
+
+// Shapes and index arrays of the row movements.
+static nvfp4_status check_move(const MoveArgs& a) {
+    if (!a.copy_row || a.tokens < 1 || a.topk < 1 || a.rows < 1 || a.cols < 1) return NVFP4_ERR_INVALID_ARG;
+    if (a.tokens >= kMaxDim || a.topk >= kMaxDim || a.rows >= kMaxDim || a.cols >= kMaxDim ||
+        a.tokens * a.topk >= kMaxDim)
+        return NVFP4_ERR_INVALID_ARG;
+    if (a.cols % 8) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned4(a.copy_row) || !aligned4(a.row_copy) || !aligned4(a.weights) || !aligned4(a.dweights) ||
+        !aligned4(a.amax))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+static nvfp4_status move_done(cudaError_t e, int launches) {
+    g_launches += launches;
+    return from_cuda(e);
+}
+
+nvfp4_status nvfp4_moe_gather(const void* x, int64_t ldx, int64_t tokens, int64_t topk, int64_t cols,
+                              const int32_t* copy_row, const int32_t* row_copy, int64_t rows, void* y, int64_t ldy,
+                              float* amax, void* stream) {
+    MoveArgs a{};
+    a.src = x;
+    a.lds = ldx;
+    a.dst = y;
+    a.ldd = ldy;
+    a.copy_row = copy_row;
+    a.row_copy = row_copy;
+    a.amax = amax;
+    a.tokens = tokens;
+    a.topk = topk;
+    a.rows = rows;
+    a.cols = cols;
+    if (!row_copy) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status st = check_move(a);
+    if (st == NVFP4_OK) st = check_bf16_matrix(x, ldx, cols);
+    if (st == NVFP4_OK) st = check_bf16_matrix(y, ldy, cols);
+    if (st != NVFP4_OK) return st;
+    int n = 0;
+    cudaError_t e = launch_moe_gather(a, static_cast<cudaStream_t>(stream), &n);
+    return move_done(e, n);
+}
+
+nvfp4_status nvfp4_moe_combine(const void* y, int64_t ldy, int64_t rows, int64_t cols, const int32_t* copy_row,
+                               const float* weights, const void* residual, int64_t ldr, int64_t tokens, int64_t topk,
+                               void* out, int64_t ldo, void* stream) {
+    MoveArgs a{};
+    a.src = y;
+    a.lds = ldy;
+    a.other = residual;
+    a.ldo = ldr;
+    a.dst = out;
+    a.ldd = ldo;
+    a.copy_row = copy_row;
+    a.weights = weights;
+    a.tokens = tokens;
+    a.topk = topk;
+    a.rows = rows;
+    a.cols = cols;
+    nvfp4_status st = check_move(a);
+    if (st == NVFP4_OK) st = check_bf16_matrix(y, ldy, cols);
+    if (st == NVFP4_OK) st = check_bf16_matrix(out, ldo, cols);
+    if (st == NVFP4_OK && residual) st = check_bf16_matrix(residual, ldr, cols);
+    if (st != NVFP4_OK) return st;
+    int n = 0;
+    cudaError_t e = launch_moe_combine(a, static_cast<cudaStream_t>(stream), &n);
+    return move_done(e, n);
+}
+
+nvfp4_status nvfp4_moe_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t ldy, int64_t tokens,
+                                    int64_t topk, int64_t cols, const int32_t* copy_row, const int32_t* row_copy,
+                                    int64_t rows, const float* weights, void* dy, int64_t lddy, float* dweights,
+                                    float* amax, void* stream) {
+    MoveArgs a{};
+    a.src = dout;
+    a.lds = ldo;
+    a.other = y;
+    a.ldo = ldy;
+    a.dst = dy;
+    a.ldd = lddy;
+    a.copy_row = copy_row;
+    a.row_copy = row_copy;
+    a.weights = weights;
+    a.dweights = dweights;
+    a.amax = amax;
+    a.tokens = tokens;
+    a.topk = topk;
+    a.rows = rows;
+    a.cols = cols;
+    if (!row_copy) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status st = check_move(a);
+    if (st == NVFP4_OK) st = check_bf16_matrix(dout, ldo, cols);
+    if (st == NVFP4_OK) st = check_bf16_matrix(dy, lddy, cols);
+    if (st == NVFP4_OK && dweights) st = check_bf16_matrix(y, ldy, cols);
+    if (st != NVFP4_OK) return st;
+    int n = 0;
+    cudaError_t e = launch_moe_combine_grad(a, static_cast<cudaStream_t>(stream), &n);
+    return move_done(e, n);
 }
 
 nvfp4_status nvfp4_scales_to_mma(const uint8_t* scales, int scale_mode, int64_t rows, int64_t k,

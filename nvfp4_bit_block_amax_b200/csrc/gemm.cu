@@ -39,12 +39,12 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace nvfp4 {
-
-__device__ unsigned int g_error_word = 0;
 
 namespace {
 
@@ -73,218 +73,7 @@ constexpr int EPI_WARPS = 8;                         // warps 2..5: scales -> TM
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC_COL = 0;
 constexpr uint32_t SF_COL = 256;                     // one buffer of 48 columns (16 SFA + 32 SFB) per stage
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
 static_assert(SF_COL + STAGES * 48 <= TMEM_COLS, "scale buffers must fit in tensor memory");
-
-// ------------------------------------------------------------- PTX wrappers --
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ unsigned long long globaltimer() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Non-blocking probe of a barrier phase.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait: false when the limit ran out (the error word and the CTA's
-// abort flag are then set) or another role already aborted.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned long long limit_ns = kWaitLimitNs) {
-    if (mbar_try(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    while (true) {
-        if (mbar_try(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > limit_ns) {
-            *abort_flag = 1;
-            atomicExch(&g_error_word, 1u);
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// NVFP4: one UE4M3 scale per 16 elements (scale_vec::4X).  MXFP4: one UE8M0
-// scale per 32 elements (scale_vec::2X), in bytes 0-1 of the same 4-byte
-// scale entry per row and 64-wide K step.
-__device__ __forceinline__ void tc_mma_nvf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate, bool mx) {
-    if (mx)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-}
-__device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
-
-// --------------------------------------------------- CTA-pair (2-SM) helpers --
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Arrive on the barrier at the same shared-memory offset in CTA `rank` of the
-// cluster.  Relaxed: what the peer waits for is tensor-memory traffic that
-// this thread has already waited out (tcgen05.wait::st / wait::ld, then
-// tcgen05.fence::before_thread_sync); a release at cluster scope would also
-// wait for every global store the warp has in flight (the epilogue's), which
-// measured above 1000 cycles per arrive.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank) {
-    asm volatile(
-        "{\n\t.reg .b32 ra;\n\t"
-        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
-        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}"
-        ::"r"(bar), "r"(rank)
-        : "memory");
-}
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_try_cluster(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    while (true) {
-        if (mbar_try_cluster(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicExch(&g_error_word, 1u);
-            return false;
-        }
-    }
-}
-// Completion of the CTA pair's prior tcgen05 operations arrives on the barrier
-// at this offset in both CTAs.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void tc_mma_nvf4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate, bool mx) {
-    if (mx)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major operand tile of rows x 128 bytes,
-// 128-byte swizzle, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
 
 // Instruction descriptor, kind::mxf4nvf4: A and B E2M1 (format 1), K-major,
 // UE4M3 scales, dense K = 64, M = 128, N = 256.
@@ -305,7 +94,27 @@ struct KParams {
     int group_m;   // tile rasterization: groups of group_m M-tiles, M fastest inside a group
     unsigned int* c_amax;   // nullable: atomic max of |C| (binary32 bits of the stored values)
     int mx;                 // MXFP4 operands: UE8M0 scales per 32 elements, no global scales (alpha = 1)
+    // The modes of the pair kernel beyond the plain product (see Mode):
+    const __nv_bfloat16* bias;      // [experts x N] or nullptr
+    const __nv_bfloat16* residual;  // [M x ldr] or nullptr
+    int64_t ldr;
+    int act;
+    __nv_bfloat16* pre;             // [M x ldp] or nullptr: also store the pre-activation
+    int64_t ldp;
+    const int* offsets;             // [experts + 1] first row (or K index) of each expert's segment
+    const int* counts;              // [experts] rows in use
+    int experts;
+    int64_t sfb_stride;             // bytes of one expert's B scales
 };
+
+// What the pair kernel computes.
+//   PLAIN     C = alpha A . B^T
+//   EPILOGUE  C = act(alpha A . B^T + bias) + residual
+//   ROWS      the same over rows of A sorted by expert, B and bias per expert;
+//             rows that belong to no token become zeros
+//   KSEG      one product per expert, C_e = alpha A . B^T over K in e's segment
+enum Mode { PLAIN, EPILOGUE, ROWS, KSEG };
+constexpr int kMaxExperts = 1024;
 
 // Fold this thread's maximum |C| (binary32 bits, non-negative) into c_amax:
 // one atomic per warp, once per kernel (the epilogue roles keep a running
@@ -336,9 +145,9 @@ __device__ __forceinline__ uint32_t packed_row_amax(const uint32_t (&packed)[64]
 // overflows -- the two global scales are applied one after the other
 // (a1 = s_global_A, a2 = s_global_B): the accumulator times one scale stays
 // in range wherever C itself does.  MXFP4 operands have no global scale.
-__device__ __forceinline__ float2 out_scales(const KParams& p) {
+__device__ __forceinline__ float2 out_scales(const KParams& p, int e = 0) {
     if (!p.a_gs) return make_float2(1.0f, 1.0f);
-    const float sa = __ldg(p.a_gs), sb = __ldg(p.b_gs);
+    const float sa = __ldg(p.a_gs), sb = __ldg(p.b_gs + e);
     const float alpha = __fmul_rn(sa, sb);
     if (alpha >= 0x1p-126f && alpha <= 0x1.fffffep127f) return make_float2(alpha, 1.0f);
     return make_float2(sa, sb);
@@ -354,15 +163,18 @@ __device__ __forceinline__ float2 scale_out2(uint32_t u0, uint32_t u1, float2 al
 // working at the same time then share group_m A panels and a few B panels,
 // which stay resident in L2, and a group starts on the B panels its
 // predecessor used last (measured: dgrad DRAM reads 3.2 -> 2.6 GB per launch).
-__device__ __forceinline__ void tile_coords(int t, const KParams& p, int& tm, int& tn) {
+__device__ __forceinline__ void tile_coords(int t, const KParams& p, int tiles_m, int& tm, int& tn) {
     const int per_group = p.group_m * p.tiles_n;
     const int g = t / per_group;
     const int r = t - g * per_group;
     const int first = g * p.group_m;
-    const int gm = min(p.group_m, p.tiles_m - first);
+    const int gm = min(p.group_m, tiles_m - first);
     tm = first + r % gm;
     tn = r / gm;
     if (g & 1) tn = p.tiles_n - 1 - tn;   // serpentine: a group starts on the B panels the previous one ended on
+}
+__device__ __forceinline__ void tile_coords(int t, const KParams& p, int& tm, int& tn) {
+    tile_coords(t, p, p.tiles_m, tm, tn);
 }
 
 // Epilogue of one column half (128 columns) of a finished tile for the
@@ -717,30 +529,21 @@ constexpr int P_OFF_MISC = P_OFF_BAR + P_NUM_BARS * 8;
 constexpr int P_OFF_EPI = (P_OFF_MISC + 16 + 1023) / 1024 * 1024;   // output staging, one 2 KB buffer per epilogue warp
 constexpr int EPI_BUF = 2048;                                      // 32 rows x 64 bytes, 64-byte swizzle
 constexpr int P_SMEM_BYTES = P_OFF_EPI + 8 * EPI_BUF + 1024;
+// The modes beyond PLAIN keep, behind that, one expert table (see Groups) and
+// the bias of each epilogue warp's 128 columns.
+constexpr int X_OFF_BIAS = P_OFF_EPI + 8 * EPI_BUF;
+constexpr int X_OFF_GROUPS = X_OFF_BIAS + 8 * 128 * 4;
+constexpr int X_SMEM_BYTES = X_OFF_GROUPS + (3 * kMaxExperts + 4) * 4 + 1024;
+static_assert(X_SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 constexpr int P_NUM_THREADS = 448;                  // 14 warps: producer, MMA, 4 scale warps, 8 epilogue warps
 // M = 256 (pair), N = 256, E2M1 x E2M1, UE4M3 scales, K-major.
 constexpr uint32_t kIdescPair = (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 
-// Output store through the tensor-memory-access unit: a 32-row x 64-byte
-// chunk staged in shared memory (64-byte swizzle: 16-byte unit u of row r
-// sits at unit u ^ ((r >> 1) & 3)) is written to C by one bulk tensor store;
-// rows and columns past the tensor's edge are dropped by the hardware.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
 // Stage one 32-row x 64-byte chunk (this lane's row: 16 words) and store it.
+// PLANES: C is a stack of matrices, the third coordinate says which.
+template <bool PLANES = false>
 __device__ __forceinline__ void store_chunk(const CUtensorMap* map_c, uint32_t buf, int lane, const uint32_t* w, int col,
-                                            int row0, bool first) {
+                                            int row0, int plane, bool first) {
     if (!first) {
         if (lane == 0) bulk_wait_read0();   // the buffer's previous chunk has been read out
         __syncwarp();
@@ -752,7 +555,8 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map_c, uint32_t b
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        tma_store_2d(map_c, buf, col, row0);
+        if constexpr (PLANES) tma_store_3d(map_c, buf, col, row0, plane);
+        else tma_store_2d(map_c, buf, col, row0);
         bulk_commit();
     }
 }
@@ -802,7 +606,7 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
         if (row0 < p.M && ncols > 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (32 * k < ncols) store_chunk(map_c, buf, lane, packed + 16 * k, col0 + 32 * k, row0, first);
+                if (32 * k < ncols) store_chunk(map_c, buf, lane, packed + 16 * k, col0 + 32 * k, row0, 0, first);
                 first = false;
             }
         }
@@ -831,7 +635,7 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
             if (live) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (32 * i + 16 * h < ncols) store_chunk(map_c, buf, lane, f + 16 * h, col0 + 32 * i + 16 * h, row0, first);
+                    if (32 * i + 16 * h < ncols) store_chunk(map_c, buf, lane, f + 16 * h, col0 + 32 * i + 16 * h, row0, 0, first);
                     first = false;
                 }
             }
@@ -841,10 +645,282 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
     return true;
 }
 
-template <bool MX>
+// ------------------------------------------------- tiles of the pair kernel --
+// Expert segments in shared memory.  offsets and counts are device data that
+// nothing has checked: here they are clamped so that every segment is a
+// non-decreasing 128-aligned range inside [0, limit) and holds its count, and
+// whatever they were, no tile leaves the operands.
+struct Groups {
+    int* first;   // [experts + 2] ROWS: first M-tile of each expert; entry `experts` is the rows behind the last one
+    int* start;   // [experts + 1]
+    int* end;     // [experts]     start + count
+};
+__device__ __forceinline__ Groups groups_at(uint8_t* smem) {
+    int* base = reinterpret_cast<int*>(smem + X_OFF_GROUPS);
+    return Groups{base, base + kMaxExperts + 2, base + 2 * kMaxExperts + 3};
+}
+// One warp fills the table (running maximum and running sum over lanes).
+__device__ __forceinline__ void fill_groups(const Groups& g, const KParams& p, int limit, int lane) {
+    int carry = 0;
+    for (int base = 0; base <= p.experts; base += 32) {
+        const int i = base + lane;
+        int v = i <= p.experts ? min(max(__ldg(p.offsets + i), 0), limit) & ~127 : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= d) v = max(v, u);
+        }
+        v = max(v, carry);
+        if (i <= p.experts) g.start[i] = v;
+        carry = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    __syncwarp();
+    carry = 0;
+    if (lane == 0) g.first[0] = 0;
+    for (int base = 0; base <= p.experts; base += 32) {
+        const int i = base + lane;
+        int n = 0;
+        if (i < p.experts) {
+            const int len = g.start[i + 1] - g.start[i];
+            g.end[i] = g.start[i] + min(max(__ldg(p.counts + i), 0), len);
+            n = (len + 255) >> 8;
+        } else if (i == p.experts) {
+            n = (limit - g.start[i] + 255) >> 8;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, n, d);
+            if (lane >= d) n += u;
+        }
+        n += carry;
+        if (i <= p.experts) g.first[i + 1] = n;
+        carry = __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+}
+
+struct Tile {
+    int m0, n0;      // first row of A and of B (inside the expert's weight)
+    int e;           // expert
+    int k0;          // first 64-wide K step
+    int k_steps;     // number of K steps; 0: nothing to multiply, C is 0
+    int row_end;     // rows at or past it are not stored ...
+    int row_live;    // ... and rows at or past this one are stored as zeros
+};
+
+template <int MODE>
+__device__ __forceinline__ int tile_count(const KParams& p, const Groups& g) {
+    if constexpr (MODE == ROWS) return g.first[p.experts + 1] * p.tiles_n;
+    if constexpr (MODE == KSEG) return p.experts * p.tiles_m * p.tiles_n;
+    return p.tiles_m * p.tiles_n;
+}
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(int t, const KParams& p, const Groups& g) {
+    Tile r;
+    int tm, tn;
+    if constexpr (MODE == ROWS) {
+        tile_coords(t, p, g.first[p.experts + 1], tm, tn);
+        int lo = 0, hi = p.experts;   // the segment that holds M-tile tm: first[lo] <= tm < first[lo + 1]
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (g.first[mid] <= tm) lo = mid;
+            else hi = mid - 1;
+        }
+        r.e = lo;
+        r.m0 = g.start[lo] + (tm - g.first[lo]) * 256;
+        r.k0 = 0;
+        if (lo < p.experts) {
+            r.row_end = g.start[lo + 1];
+            r.row_live = g.end[lo];
+        } else {                      // behind the last segment
+            r.row_end = p.M;
+            r.row_live = 0;
+        }
+        r.k_steps = r.m0 < r.row_live ? p.K / 64 : 0;
+    } else if constexpr (MODE == KSEG) {
+        const int per = p.tiles_m * p.tiles_n;
+        r.e = t / per;
+        tile_coords(t - r.e * per, p, tm, tn);
+        r.m0 = tm * 256;
+        r.k0 = g.start[r.e] >> 6;
+        r.k_steps = (g.end[r.e] - g.start[r.e] + 63) >> 6;
+        r.row_end = r.row_live = p.M;
+    } else {
+        tile_coords(t, p, tm, tn);
+        r.e = 0;
+        r.m0 = tm * 256;
+        r.k0 = 0;
+        r.k_steps = p.K / 64;
+        r.row_end = r.row_live = p.M;
+    }
+    r.n0 = tn * 256;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// v[j] += residual[j], 32 values of a row of which `n` are inside the matrix.
+// The row starts on a 16-byte boundary and so does every group of 8; columns
+// past the matrix's edge are not touched, they may lie past the allocation.
+__device__ __forceinline__ void add_residual(float (&v)[32], const __nv_bfloat16* r, int n) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        if (8 * g + 8 <= n) {
+            const uint4 w = *reinterpret_cast<const uint4*>(r + 8 * g);
+            v[8 * g] += bf16_lo(w.x);
+            v[8 * g + 1] += bf16_hi(w.x);
+            v[8 * g + 2] += bf16_lo(w.y);
+            v[8 * g + 3] += bf16_hi(w.y);
+            v[8 * g + 4] += bf16_lo(w.z);
+            v[8 * g + 5] += bf16_hi(w.z);
+            v[8 * g + 6] += bf16_lo(w.w);
+            v[8 * g + 7] += bf16_hi(w.w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * g + e < n) v[8 * g + e] += __bfloat162float(r[8 * g + e]);
+        }
+    }
+}
+
+// Store a chunk of which only the first n columns lie inside the matrix.  A
+// bulk tensor store writes whole 16-byte units (the columns past the edge in
+// the last one as zeros), so a chunk that ends inside one goes out with plain
+// stores: what lies behind the matrix's columns stays as it was.
+template <typename T, bool PLANES>
+__device__ __forceinline__ void put_chunk(const CUtensorMap* map, T* base, int64_t ld, uint32_t buf, int lane,
+                                          const uint32_t (&w)[16], int col, int n, int row0, int row_end, int64_t plane_rows,
+                                          int plane, bool& first) {
+    constexpr int kUnit = 16 / sizeof(T);
+    if (n >= 4 * kUnit || n % kUnit == 0) {
+        store_chunk<PLANES>(map, buf, lane, w, col, row0, plane, first);
+        first = false;
+    } else if (row0 + lane < row_end) {
+        T* p = base + (plane * plane_rows + row0 + lane) * ld + col;
+#pragma unroll
+        for (int j = 0; j < 4 * kUnit; ++j)
+            if (j < n) {
+                if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
+                else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            }
+    }
+}
+
+// Epilogue of the modes beyond PLAIN, one column half of a tile for the
+// calling warp's 32 rows: per 32 columns TMEM -> registers, scales and bias,
+// pre-activation out, activation, residual, out.  The pre-activation is
+// rounded to bf16 where it is stored; the activation takes the binary32 value,
+// so C is rounded once.
+template <int MODE>
+__device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, int half, int q, int lane, uint32_t rank,
+                                             uint32_t tmem, uint32_t bar_tfull, uint32_t bar_tempty,
+                                             uint32_t& acc_phase, volatile int* abort_flag, uint32_t& amax_acc,
+                                             const CUtensorMap* map_c, const CUtensorMap* map_pre, uint32_t buf,
+                                             float* s_bias, bool& first) {
+    const int row0 = t.m0 + (int)rank * 128 + q * 32, row = row0 + lane;
+    const int col0 = t.n0 + half * 128;
+    const int ncols = p.N - col0;
+    const bool store = row0 < t.row_end && ncols > 0;
+    const bool on = row < t.row_live;
+    const int plane = MODE == KSEG ? t.e : 0;
+    const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + ACC_COL + half * 128;
+    const float2 alpha = out_scales(p, MODE == ROWS ? min(t.e, p.experts - 1) : 0);
+    if (MODE != KSEG && p.bias) {
+        const __nv_bfloat16* b = p.bias + (int64_t)min(t.e, p.experts - 1) * p.N + col0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s_bias[32 * c + lane] = 32 * c + lane < ncols ? __bfloat162float(b[32 * c + lane]) : 0.0f;
+        __syncwarp();
+    }
+    if (!mbar_wait_cluster(bar_tfull, acc_phase, abort_flag)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float v[32];
+        if (t.k_steps) {
+            uint32_t u[32];
+            tc_ld_32x32b_x32(taddr + 32 * i, u);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float2 f = scale_out2(u[2 * j], u[2 * j + 1], alpha);
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        }
+        if (i == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(bar_tempty);
+                else mbar_arrive_cluster(bar_tempty, 0);
+            }
+            acc_phase ^= 1;
+        }
+        if (!store || 32 * i >= ncols) continue;
+        uint32_t w[16];
+        if constexpr (MODE != KSEG) {
+            if (p.bias) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 b = *reinterpret_cast<const float4*>(s_bias + 32 * i + 4 * j);
+                    v[4 * j] += b.x;
+                    v[4 * j + 1] += b.y;
+                    v[4 * j + 2] += b.z;
+                    v[4 * j + 3] += b.w;
+                }
+            }
+            if (p.pre) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = on ? pack_bf16(v[2 * j], v[2 * j + 1]) : 0u;
+                put_chunk<__nv_bfloat16, false>(map_pre, p.pre, p.ldp, buf, lane, w, col0 + 32 * i, ncols - 32 * i, row0,
+                                                t.row_end, 0, 0, first);
+            }
+            apply_act(p.act, v);
+            if (p.residual && on) add_residual(v, p.residual + (int64_t)row * p.ldr + col0 + 32 * i, ncols - 32 * i);
+        }
+        if (p.out_bf16) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                w[j] = on ? pack_bf16(v[2 * j], v[2 * j + 1]) : 0u;
+                const int c = 32 * i + 2 * j;
+                m = absmax2(m, c + 1 < ncols ? w[j] : c < ncols ? w[j] & 0xFFFFu : 0u);
+            }
+            amax_acc = max(amax_acc, absmax2_fold(m));
+            put_chunk<__nv_bfloat16, MODE == KSEG>(map_c, reinterpret_cast<__nv_bfloat16*>(p.c), p.ldc, buf, lane, w,
+                                                   col0 + 32 * i, ncols - 32 * i, row0, t.row_end, p.M, plane, first);
+        } else {
+            float fmax = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float f = on ? v[16 * h + j] : 0.0f;
+                    w[j] = __float_as_uint(f);
+                    if (32 * i + 16 * h + j < ncols) fmax = fmaxf(fmax, fabsf(f));
+                }
+                if (32 * i + 16 * h < ncols)
+                    put_chunk<float, MODE == KSEG>(map_c, reinterpret_cast<float*>(p.c), p.ldc, buf, lane, w,
+                                                   col0 + 32 * i + 16 * h, ncols - 32 * i - 16 * h, row0, t.row_end, p.M,
+                                                   plane, first);
+            }
+            amax_acc = max(amax_acc, __float_as_uint(fmax));
+        }
+    }
+    __syncwarp();   // s_bias has been read
+    return true;
+}
+
+template <bool MX, int MODE>
 __global__ void __launch_bounds__(P_NUM_THREADS, 1)
 gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_c, KParams p) {
+                      const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pre,
+                      KParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -860,9 +936,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
-    const int num_tiles = p.tiles_m * p.tiles_n;
-    const int k_blocks = (p.K + BK - 1) / BK;
-    const int k_steps = p.K / 64;
+    const Groups groups = groups_at(smem);   // MODE ROWS and KSEG only
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P_STAGES; ++s) {
@@ -877,6 +951,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    if ((MODE == ROWS || MODE == KSEG) && warp == 2) fill_groups(groups, p, MODE == ROWS ? p.M : p.K, lane);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS));
@@ -887,6 +962,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const int num_tiles = tile_count<MODE>(p, groups);
 
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
@@ -896,10 +972,13 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
             bool ok = true;
             const int rc_a_max = (p.M + 127) >> 7, rc_b_max = (p.N + 127) >> 7;
             for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
-                int tm, tn;
-                tile_coords(tile, p, tm, tn);
-                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
-                const int rc_a = m0 >> 7, rc_b = (tn * 256) >> 7;
+                const Tile t = tile_at<MODE>(tile, p, groups);
+                const int k_steps = t.k_steps, k_blocks = (k_steps + 3) >> 2;
+                // ROWS: B holds the experts' weights one after another, N rows each (a row past the
+                // expert's last one is another expert's or zero-filled, and its column is not stored)
+                const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * 128 + (MODE == ROWS ? t.e * p.N : 0);
+                const int rc_a = m0 >> 7, rc_b = t.n0 >> 7;
+                const uint8_t* sfb = p.sfb + (MODE == ROWS ? (int64_t)t.e * p.sfb_stride : 0);
                 const int has_a = rc_a < rc_a_max ? 1 : 0;
                 const int nh = (rc_b + 1 < rc_b_max) ? 2 : 1;
                 for (int kb = 0; kb < k_blocks; ++kb) {
@@ -907,14 +986,14 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
                     const int nk = min(4, k_steps - kb * 4);
                     const uint32_t full = bar_full + 8 * s;
                     mbar_expect_tx(full, (uint32_t)(P_A_STAGE + P_B_STAGE + nk * 512 * (has_a + nh)));
-                    tma_load_2d(sbase + P_OFF_A + s * P_A_STAGE, &map_a, full, kb * BKB, m0);
-                    tma_load_2d(sbase + P_OFF_B + s * P_B_STAGE, &map_b, full, kb * BKB, n0);
+                    tma_load_2d(sbase + P_OFF_A + s * P_A_STAGE, &map_a, full, t.k0 * 32 + kb * BKB, m0);
+                    tma_load_2d(sbase + P_OFF_B + s * P_B_STAGE, &map_b, full, t.k0 * 32 + kb * BKB, n0);
                     if (has_a)
                         bulk_load(sbase + P_OFF_SFA + s * SFA_STAGE,
-                                  p.sfa + ((int64_t)rc_a * p.chunks_k + kb * 4) * 512, nk * 512, full);
+                                  p.sfa + ((int64_t)rc_a * p.chunks_k + t.k0 + kb * 4) * 512, nk * 512, full);
                     for (int h = 0; h < nh; ++h)
                         bulk_load(sbase + P_OFF_SFB + s * SFB_STAGE + h * 2048,
-                                  p.sfb + ((int64_t)(rc_b + h) * p.chunks_k + kb * 4) * 512, nk * 512, full);
+                                  sfb + ((int64_t)(rc_b + h) * p.chunks_k + t.k0 + kb * 4) * 512, nk * 512, full);
                     issued_any |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
                     if (++s == P_STAGES) { s = 0; phase ^= 1; }
@@ -935,6 +1014,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
             bool ok = true;
             const uint32_t idesc = kIdescPair | (MX ? kIdescUe8m0 : 0u);
             for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
+                const int k_steps = tile_at<MODE>(tile, p, groups).k_steps, k_blocks = (k_steps + 3) >> 2;
                 if (!mbar_wait_cluster(bar_tempty, acc_phase ^ 1, abort_flag)) break;
                 tc_fence_after();
                 for (int kb = 0; kb < k_blocks; ++kb) {
@@ -977,6 +1057,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
+            const int k_blocks = (tile_at<MODE>(tile, p, groups).k_steps + 3) >> 2;
             for (int kb = 0; kb < k_blocks; ++kb) {
                 if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
                 const uint32_t sfa_s = sbase + P_OFF_SFA + s * SFA_STAGE + 16 * lane;
@@ -1016,14 +1097,22 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         // warps 6..9: columns 0..127, warps 10..13: columns 128..255, of the
         // TMEM lane quarter warp % 4
         const int q = warp & 3, half = (warp - 6) >> 2;
-        const float2 alpha = out_scales(p);
+        const float2 alpha = MODE == PLAIN ? out_scales(p, 0) : make_float2(0.0f, 0.0f);
         const uint32_t buf = sbase + P_OFF_EPI + (warp - 6) * EPI_BUF;
         uint32_t acc_phase = 0;
         uint32_t amax_acc = 0;
         bool first = true;
-        for (int tile = cluster; tile < num_tiles; tile += n_clusters)
-            if (!epilogue_half_pair(p, tile, half, q, lane, rank, tmem, alpha, bar_tfull, bar_tempty, acc_phase,
-                                    abort_flag, amax_acc, &map_c, buf, first)) break;
+        for (int tile = cluster; tile < num_tiles; tile += n_clusters) {
+            if constexpr (MODE == PLAIN) {
+                if (!epilogue_half_pair(p, tile, half, q, lane, rank, tmem, alpha, bar_tfull, bar_tempty, acc_phase,
+                                        abort_flag, amax_acc, &map_c, buf, first)) break;
+            } else {
+                float* s_bias = reinterpret_cast<float*>(smem + X_OFF_BIAS) + (warp - 6) * 128;
+                if (!epilogue_ext<MODE>(p, tile_at<MODE>(tile, p, groups), half, q, lane, rank, tmem, bar_tfull,
+                                        bar_tempty, acc_phase, abort_flag, amax_acc, &map_c, &map_pre, buf, s_bias,
+                                        first)) break;
+            }
+        }
         if (lane == 0) bulk_wait0();    // every store of this warp has completed
         __syncwarp();
         if (p.c_amax) amax_publish(p.c_amax, amax_acc);
@@ -1084,15 +1173,16 @@ bool make_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t k,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ldc, bool bf16) {
+// planes > 0: a stack of `planes` such matrices.
+bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ldc, bool bf16, int64_t planes = 0) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int esz = bf16 ? 2 : 4;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(ldc * esz)};
-    cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)(ldc * esz), (cuuint64_t)(rows * ldc * esz)};
+    cuuint32_t box[3] = {(cuuint32_t)(64 / esz), 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes ? 3 : 2, base, dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1115,8 +1205,13 @@ DeviceInfo device_info() {
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         for (auto k : {gemm_nvf4_kernel<false>, gemm_nvf4_kernel<true>})
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-        for (auto k : {gemm_nvf4_pair_kernel<false>, gemm_nvf4_pair_kernel<true>}) {
+        for (auto k : {gemm_nvf4_pair_kernel<false, PLAIN>, gemm_nvf4_pair_kernel<true, PLAIN>}) {
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_BYTES);
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
+        }
+        for (auto k : {gemm_nvf4_pair_kernel<false, EPILOGUE>, gemm_nvf4_pair_kernel<false, ROWS>,
+                       gemm_nvf4_pair_kernel<false, KSEG>}) {
+            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, X_SMEM_BYTES);
             cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
         }
         cudaLaunchConfig_t cfg = {};
@@ -1131,7 +1226,7 @@ DeviceInfo device_info() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, gemm_nvf4_pair_kernel<false>, &cfg) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveClusters(&clusters, gemm_nvf4_pair_kernel<false, PLAIN>, &cfg) != cudaSuccess ||
             clusters < 1) {
             cudaGetLastError();
             clusters = n / 2;
@@ -1149,6 +1244,25 @@ int group_for(int64_t rows_per_tile, int64_t K, int tiles_m) {
     if (gm < 1) gm = 1;
     if (gm > tiles_m) gm = tiles_m;
     return (int)gm;
+}
+
+typedef void (*PairKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, KParams);
+
+cudaError_t launch_pairs(PairKernel kernel, int clusters, int smem, cudaStream_t s, const CUtensorMap& ma,
+                         const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mp, const KParams& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters);
+    cfg.blockDim = dim3(P_NUM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, mp, p);
 }
 
 }  // namespace
@@ -1195,20 +1309,52 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
     p.group_m = group_for(256, g.K, p.tiles_m);
     const int tiles = p.tiles_m * p.tiles_n;
     const int clusters = tiles < dev.pair_clusters ? tiles : dev.pair_clusters;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(P_NUM_THREADS);
-    cfg.dynamicSmemBytes = P_SMEM_BYTES;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return p.mx ? cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<true>, ma, mb, mc, p)
-                : cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<false>, ma, mb, mc, p);
+    return p.mx ? launch_pairs(gemm_nvf4_pair_kernel<true, PLAIN>, clusters, P_SMEM_BYTES, s, ma, mb, mc, mc, p)
+                : launch_pairs(gemm_nvf4_pair_kernel<false, PLAIN>, clusters, P_SMEM_BYTES, s, ma, mb, mc, mc, p);
+}
+
+cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
+    const DeviceInfo dev = device_info();
+    KParams p{};
+    p.sfa = g.sfa;
+    p.sfb = g.sfb;
+    p.a_gs = g.a_gs;
+    p.b_gs = g.b_gs;
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.K = (int)g.K;
+    p.chunks_k = (int)mma_chunks_k(g.K);
+    p.out_bf16 = g.out_bf16;
+    p.c_amax = reinterpret_cast<unsigned int*>(g.c_amax);
+    p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+    p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+    p.ldr = g.ldr;
+    p.act = g.act;
+    p.pre = static_cast<__nv_bfloat16*>(g.pre);
+    p.ldp = g.ldp;
+    p.c = g.c;
+    p.ldc = g.ldc;
+    p.offsets = g.offsets;
+    p.counts = g.counts;
+    p.experts = g.offsets ? (int)g.experts : 1;
+    p.sfb_stride = (int64_t)mma_scale_bytes(g.N, g.K);
+    p.tiles_n = (int)ceil_div(g.N, BN);
+    const bool rows = g.offsets && !g.wgrad;
+    CUtensorMap ma, mb, mc, mp;
+    if (!make_code_map(&ma, g.a, g.M, g.K, 128) || !make_code_map(&mb, g.b, rows ? g.experts * g.N : g.N, g.K, 128) ||
+        !make_out_map(&mc, g.c, g.M, g.N, g.ldc, g.out_bf16 != 0, g.wgrad ? g.experts : 0) ||
+        (g.pre && !make_out_map(&mp, g.pre, g.M, g.N, g.ldp, true)))
+        return cudaErrorInvalidValue;
+    if (!g.pre) mp = mc;
+    p.tiles_m = (int)ceil_div(g.M, 256);
+    p.group_m = group_for(256, g.wgrad ? ceil_div(g.K, g.experts) : g.K, p.tiles_m);   // an average segment
+    // ROWS: how the rows fall into segments is known on the device only; at
+    // most, every 128 rows are a tile of their own.
+    const int64_t tiles = (rows ? ceil_div(g.M, 128) : p.tiles_m) * p.tiles_n * (g.wgrad ? g.experts : 1);
+    const int clusters = (int)(tiles < dev.pair_clusters ? tiles : dev.pair_clusters);
+    auto kernel = g.wgrad ? gemm_nvf4_pair_kernel<false, KSEG>
+                          : rows ? gemm_nvf4_pair_kernel<false, ROWS> : gemm_nvf4_pair_kernel<false, EPILOGUE>;
+    return launch_pairs(kernel, clusters, X_SMEM_BYTES, s, ma, mb, mc, mp, p);
 }
 
 unsigned int read_and_clear_error_word(cudaStream_t s, cudaError_t* err) {

@@ -66,6 +66,84 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s);
 
+// The linear layer's product (see nvfp4.h): a dense one (offsets null), one
+// per expert over sorted rows, or (wgrad) one per expert over segments of K.
+struct GemmExtArgs {
+    const uint8_t* a;
+    const uint8_t* sfa;
+    const float* a_gs;
+    const uint8_t* b;
+    const uint8_t* sfb;
+    const float* b_gs;
+    int64_t M, N, K;
+    const void* bias;             // bf16, nullable
+    int act;
+    const void* residual;         // bf16, nullable
+    int64_t ldr;
+    int out_bf16;
+    void* c;
+    int64_t ldc;
+    void* pre;                    // bf16, nullable
+    int64_t ldp;
+    float* c_amax;                // nullable, zeroed by the caller
+    const int32_t* offsets;       // nullable
+    const int32_t* counts;
+    int64_t experts;
+    int wgrad;
+};
+cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s);
+constexpr int64_t kMaxExpertsArg = 1024;
+
+struct ActGradArgs {
+    const void* dy;
+    int64_t ldy;
+    const void* z;
+    int64_t ldz;
+    int64_t M, N;
+    int act;
+    const int32_t* offsets;       // nullable
+    const int32_t* counts;
+    int64_t experts;
+    void* dz;
+    int64_t lddz;
+    float* dbias;                 // nullable
+    float* amax;                  // nullable
+    float* workspace;             // [ceil(M / 128) x N], with dbias
+};
+cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches);
+
+struct SortArgs {
+    const int32_t* ids;
+    int64_t n, experts, rows;
+    int32_t* offsets;
+    int32_t* counts;
+    int32_t* row_copy;
+    int32_t* copy_row;
+    int32_t* workspace;
+};
+size_t moe_sort_workspace(int64_t n, int64_t experts);
+cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t s, int* launches);
+
+// One struct for the three row movements: src -> dst, with `other` the
+// residual (combine) or the forward rows (combine's gradient).
+struct MoveArgs {
+    const void* src;
+    int64_t lds;
+    const void* other;
+    int64_t ldo;
+    void* dst;
+    int64_t ldd;
+    const int32_t* copy_row;
+    const int32_t* row_copy;
+    const float* weights;
+    float* dweights;
+    float* amax;
+    int64_t tokens, topk, rows, cols;
+};
+cudaError_t launch_moe_gather(const MoveArgs& a, cudaStream_t s, int* launches);
+cudaError_t launch_moe_combine(const MoveArgs& a, cudaStream_t s, int* launches);
+cudaError_t launch_moe_combine_grad(const MoveArgs& a, cudaStream_t s, int* launches);
+
 unsigned int read_and_clear_error_word(cudaStream_t s, cudaError_t* err);
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 cudaError_t launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,

@@ -1,0 +1,665 @@
+// layer.cu -- what surrounds the GEMMs of a linear layer and of a layer of
+// experts: the activation's gradient with the bias gradient, the sort of
+// token copies by expert, and the row movements there and back.
+//
+// All of it is bound by HBM (the sort by latency): every matrix element is
+// read once and written once, in 16-byte vectors with several loads in flight
+// per thread.  Sums are binary32 in a fixed order (no atomics), so results
+// repeat bit for bit; the only atomics are maxima of |x|, which do not depend
+// on their order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "activation.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// 16-byte load of data that may be overwritten in place by the same thread.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+    f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x);
+    f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+    f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z);
+    f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+__device__ __forceinline__ uint32_t absmax8(uint32_t acc, const uint4& w) {
+    return absmax2(absmax2(absmax2(absmax2(acc, w.x), w.y), w.z), w.w);
+}
+
+// Fold every thread's packed |bf16| maximum into *amax (binary32, zeroed by
+// the caller): one atomic per CTA, none where the word is already as large.
+__device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
+    __shared__ uint32_t s_max[kWarps];
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, absmax2_fold(acc));
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t b = 0;
+        for (int w = 0; w < kWarps; ++w) b = max(b, s_max[w]);
+        uint32_t* word = reinterpret_cast<uint32_t*>(amax);
+        if (b > *reinterpret_cast<volatile uint32_t*>(word)) atomicMax(word, b);
+    }
+}
+
+// ------------------------------------------------------ activation gradient --
+// dz = dy * act'(z) and the column sums of dz.  A CTA takes 128 rows x 256
+// columns (128 rows: no tile crosses an expert's segment), a warp 16 of the
+// rows, a lane 8 columns.  6 bytes per element moved; the sums of the 128
+// rows go to the workspace, [row tiles x N] binary32 (1/64 of the bytes), and
+// bias_grad_kernel adds them up in order.
+constexpr int kRowTile = 128, kColTile = 256;
+
+struct ActGradParams {
+    const __nv_bfloat16* dy;
+    const __nv_bfloat16* z;
+    __nv_bfloat16* dz;
+    int64_t ldy, ldz, lddz;
+    int64_t M, N;
+    int64_t strips;        // ceil(N / kColTile)
+    const int* offsets;    // nullable: rows in expert segments
+    const int* counts;
+    int experts;
+    float* sums;           // [row tiles x N], or dbias itself when one row tile is all there is; nullable
+    float* amax;           // nullable
+};
+
+// Rows of the row tile at m0 that belong to tokens: all of M, or those inside
+// the segment that covers the tile.  offsets are unchecked device data; the
+// result lies in [m0, M] whatever they hold.
+__device__ __forceinline__ int64_t live_rows(const int* offsets, const int* counts, int experts, int64_t m0, int64_t M) {
+    if (!offsets) return M;
+    int lo = 0, hi = experts;   // last entry with offsets[lo] <= m0
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(offsets + mid) <= m0) lo = mid;
+        else hi = mid - 1;
+    }
+    if (lo >= experts) return m0;
+    const int64_t end = min((int64_t)__ldg(offsets + lo) + __ldg(counts + lo), (int64_t)__ldg(offsets + lo + 1));
+    return max(m0, min(end, M));
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
+    __shared__ float s_sum[kWarps][kColTile];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tile = blockIdx.x / p.strips, strip = blockIdx.x - tile * p.strips;   // columns fastest
+    const int64_t m0 = tile * kRowTile, col = strip * kColTile + 8 * lane;
+    const int64_t stop = min(m0 + kRowTile, p.M);                                // rows to write
+    const int64_t live = min(live_rows(p.offsets, p.counts, p.experts, m0, p.M), stop);   // rows to compute
+    const int64_t n = p.N - col;
+    float sum[8] = {};
+    uint32_t peak = 0;
+    constexpr int U = 4;
+    for (int64_t r0 = m0 + warp; r0 < stop; r0 += U * kWarps) {
+        uint4 g[U], z[U];
+        if (n >= 8) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * kWarps;
+                g[u] = z[u] = make_uint4(0, 0, 0, 0);
+                if (r < live) {
+                    g[u] = ld_stream(p.dy + r * p.ldy + col);
+                    if (ACT != ACT_NONE) z[u] = ld_stream(p.z + r * p.ldz + col);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * kWarps;
+                if (r >= stop) break;
+                float a[8], b[8];
+                unpack8(g[u], a);
+                unpack8(z[u], b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    a[e] = act_grad_value<ACT>(a[e], b[e]);
+                    if (r >= live) a[e] = 0.0f;
+                    sum[e] += a[e];
+                }
+                const uint4 o = pack8(a);
+                peak = absmax8(peak, o);
+                *reinterpret_cast<uint4*>(p.dz + r * p.lddz + col) = o;
+            }
+        } else if (n > 0) {
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * kWarps;
+                if (r >= stop) break;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) {
+                        float v = 0.0f;
+                        if (r < live)
+                            v = act_grad_value<ACT>(__bfloat162float(p.dy[r * p.ldy + col + e]),
+                                                    ACT == ACT_NONE ? 0.0f : __bfloat162float(p.z[r * p.ldz + col + e]));
+                        sum[e] += v;
+                        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                        peak = absmax2(peak, (uint32_t)__bfloat16_as_ushort(h));
+                        p.dz[r * p.lddz + col + e] = h;
+                    }
+            }
+        }
+    }
+    if (p.sums) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[warp][8 * lane + e] = sum[e];
+        __syncthreads();
+        const int64_t c = strip * kColTile + threadIdx.x;
+        if (c < p.N) {
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) t += s_sum[w][threadIdx.x];
+            p.sums[tile * p.N + c] = t;
+        }
+    }
+    if (p.amax) publish_amax(p.amax, peak);
+}
+
+// dbias [experts x N] from the sums of the row tiles: 64 columns per CTA, the
+// tiles of a segment dealt to 4 threads per column, then added in order.
+__global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __restrict__ sums, int64_t M, int64_t N,
+                                                             const int* offsets, const int* counts, float* dbias) {
+    __shared__ float s[4][64];
+    const int e = blockIdx.y, part = threadIdx.x >> 6, c = threadIdx.x & 63;
+    const int64_t col = (int64_t)blockIdx.x * 64 + c;
+    const int64_t tiles = (M + kRowTile - 1) / kRowTile;
+    int64_t first = 0, last = tiles;
+    if (offsets) {
+        const int64_t o = __ldg(offsets + e);
+        const int64_t end = min(o + __ldg(counts + e), (int64_t)__ldg(offsets + e + 1));
+        first = max(o, (int64_t)0) / kRowTile;
+        last = min(tiles, (end + kRowTile - 1) / kRowTile);
+    }
+    float t = 0.0f;
+    if (col < N) {
+#pragma unroll 8
+        for (int64_t i = first + part; i < last; i += 4) t += __ldg(sums + i * N + col);
+    }
+    s[part][c] = t;
+    __syncthreads();
+    if (part == 0 && col < N) dbias[(int64_t)e * N + col] = (s[0][c] + s[1][c]) + (s[2][c] + s[3][c]);
+}
+
+// ------------------------------------------------------------ sort by expert --
+// A stable counting sort of n copies by expert.  The copies are dealt to CTAs
+// in consecutive chunks, to a CTA's warps in consecutive parts, to a warp's
+// lanes 32 at a time; a copy's rank among its expert's is the sum of what came
+// before on each of these levels, so it depends on the input alone.
+struct SortParams {
+    const int* ids;       // [n]
+    int n, experts, rows;
+    int chunk;            // copies per CTA, a multiple of kThreads
+    int* hist;            // [CTAs x experts], only with more than one CTA
+    int* offsets;
+    int* counts;
+    int* row_copy;        // [rows]
+    int* copy_row;        // [n]
+};
+
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(SortParams p) {
+    extern __shared__ int s_count[];
+    for (int e = threadIdx.x; e < p.experts; e += kThreads) s_count[e] = 0;
+    __syncthreads();
+    const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.n);
+    for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
+        const int e = __ldg(p.ids + i);
+        if (e >= 0 && e < p.experts) atomicAdd(s_count + e, 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kThreads) p.hist[(int64_t)blockIdx.x * p.experts + e] = s_count[e];
+}
+
+__global__ void __launch_bounds__(kThreads) sort_place_kernel(SortParams p) {
+    extern __shared__ int s_mem[];
+    int* s_at = s_mem;                              // [warps x experts] next row of each warp's copies of an expert
+    int* s_off = s_mem + kWarps * p.experts;        // [experts + 1]
+    int* s_total = s_off + p.experts + 1;           // [experts]
+    __shared__ int s_scan[kWarps], s_carry;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kWarps * p.experts; i += kThreads) s_at[i] = 0;
+    if (threadIdx.x == 0) s_carry = 0;
+    __syncthreads();
+    // this CTA's copies, counted per warp
+    const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.n);
+    const int part = p.chunk / kWarps;
+    const int64_t wb = begin + (int64_t)warp * part, we = min(wb + part, end);
+    for (int64_t i = wb + lane; i < we; i += 32) {
+        const int e = __ldg(p.ids + i);
+        if (e >= 0 && e < p.experts) atomicAdd(s_at + warp * p.experts + e, 1);
+    }
+    __syncthreads();
+    // per expert: the total over all CTAs, and where this CTA's first copy goes among them
+    for (int base = 0; base < p.experts; base += kThreads) {
+        const int e = base + threadIdx.x;
+        int before = 0, total = 0;
+        if (e < p.experts) {
+            if (gridDim.x == 1) {
+                for (int w = 0; w < kWarps; ++w) total += s_at[w * p.experts + e];
+            } else {
+#pragma unroll 4
+                for (int b = 0; b < (int)gridDim.x; ++b) {
+                    const int h = __ldg(p.hist + (int64_t)b * p.experts + e);
+                    total += h;
+                    if (b < (int)blockIdx.x) before += h;
+                }
+            }
+            s_total[e] = total;
+        }
+        // exclusive running sum of the padded totals over the CTA's threads
+        const int padded = (total + 127) & ~127;
+        int incl = padded;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += u;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int lead = s_carry;
+        for (int w = 0; w < warp; ++w) lead += s_scan[w];
+        if (e < p.experts) {
+            s_off[e] = lead + incl - padded;
+            int at = s_off[e] + before;
+            for (int w = 0; w < kWarps; ++w) {
+                const int c = s_at[w * p.experts + e];
+                s_at[w * p.experts + e] = at;
+                at += c;
+            }
+            if (e == p.experts - 1) s_off[p.experts] = lead + incl;
+        }
+        __syncthreads();
+        if (threadIdx.x == kThreads - 1) s_carry = lead + incl;
+        __syncthreads();
+    }
+    // offsets and counts, no further than the rows there are
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e <= p.experts; e += kThreads) {
+            const int o = min(s_off[e], p.rows);
+            p.offsets[e] = o;
+            if (e < p.experts) p.counts[e] = min(s_total[e], min(s_off[e + 1], p.rows) - o);
+        }
+    }
+    // place the copies
+    for (int64_t i0 = wb; i0 < we; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int e = i < we ? __ldg(p.ids + i) : -1;
+        const bool ok = e >= 0 && e < p.experts;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? e : -1);
+        int row = -1;
+        if (ok) row = s_at[warp * p.experts + e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (ok && (same >> lane) == 1u) s_at[warp * p.experts + e] = row + 1;   // the last of its kind
+        __syncwarp();
+        if (row >= p.rows) row = -1;
+        if (i < we) p.copy_row[i] = row;
+        if (row >= 0) p.row_copy[row] = (int)i;
+    }
+    // rows without a copy
+    for (int e = blockIdx.x; e <= p.experts; e += gridDim.x) {
+        const int from = min(e < p.experts ? s_off[e] + s_total[e] : s_off[e], p.rows);
+        const int to = e < p.experts ? min(s_off[e + 1], p.rows) : p.rows;
+        for (int r = from + threadIdx.x; r < to; r += kThreads) p.row_copy[r] = -1;
+    }
+}
+
+// -------------------------------------------------------- rows there and back --
+struct MoveParams {
+    const __nv_bfloat16* src;       // gather: x; combine: y; gradient: dout
+    const __nv_bfloat16* other;     // combine: residual (nullable); gradient: y (nullable)
+    __nv_bfloat16* dst;             // gather: sorted rows; combine: out; gradient: dy
+    int64_t lds, ldo, ldd;
+    const int* copy_row;            // [tokens x topk]
+    const int* row_copy;            // [rows]
+    const float* weights;           // [tokens x topk], nullable: 1
+    float* dweights;                // gradient, nullable
+    float* amax;                    // nullable
+    int64_t tokens, rows, cols;
+    int topk;
+};
+
+__device__ __forceinline__ int row_of(const MoveParams& p, int64_t copy) {
+    const int r = __ldg(p.copy_row + copy);
+    return r >= 0 && r < p.rows ? r : -1;
+}
+
+// Rows that hold no copy become zeros: one warp looks at 32 rows x 1024 columns.
+__device__ __forceinline__ int64_t zero_units(const MoveParams& p) {
+    return (p.rows + 31) / 32 * ((p.cols + 1023) / 1024);
+}
+__device__ __forceinline__ void zero_unit(const MoveParams& p, int64_t unit, int lane) {
+    const int64_t groups = (p.rows + 31) / 32;
+    const int64_t r0 = unit % groups * 32, c0 = unit / groups * 1024;
+    bool empty = false;
+    if (r0 + lane < p.rows) {
+        const int c = __ldg(p.row_copy + r0 + lane);
+        empty = c < 0 || c >= p.tokens * p.topk;
+    }
+    unsigned todo = __ballot_sync(0xFFFFFFFFu, empty);
+    while (todo) {
+        const int64_t r = r0 + __ffs(todo) - 1;
+        todo &= todo - 1;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int64_t c = c0 + 256 * v + 8 * lane;
+            if (c < p.cols) *reinterpret_cast<uint4*>(p.dst + r * p.ldd + c) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// Sorted rows from token rows.  A warp takes 1024 columns of one token: reads
+// them once, 4 loads in flight per lane, and writes them topk times.
+__global__ void __launch_bounds__(kThreads) gather_kernel(MoveParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t segs = (p.cols + 1023) / 1024, units = p.tokens * segs, all = units + zero_units(p);
+    uint32_t peak = 0;
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < all; u += (int64_t)gridDim.x * kWarps) {
+        if (u >= units) {
+            zero_unit(p, u - units, lane);
+            continue;
+        }
+        const int64_t t = u / segs, c0 = (u - t * segs) * 1024 + 8 * lane;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = c0 + 256 * i < p.cols ? ldg_stream(p.src + t * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
+        bool used = false;
+        for (int j = 0; j < p.topk; ++j) {
+            const int r = row_of(p, t * p.topk + j);
+            if (r < 0) continue;
+            used = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c0 + 256 * i < p.cols) *reinterpret_cast<uint4*>(p.dst + r * p.ldd + c0 + 256 * i) = v[i];
+        }
+        if (used) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) peak = absmax8(peak, v[i]);
+        }
+    }
+    if (p.amax) publish_amax(p.amax, peak);
+}
+
+// Token rows from sorted rows: a warp takes 512 columns of one token, the rows
+// of 4 copies in flight at a time, and sums in the order of the copies.
+__global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t segs = (p.cols + 511) / 512, units = p.tokens * segs;
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
+        const int64_t t = u / segs, c0 = (u - t * segs) * 512 + 8 * lane;
+        const bool in[2] = {c0 < p.cols, c0 + 256 < p.cols};
+        float acc[2][8] = {};
+        uint4 res[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            res[i] = p.other && in[i] ? ld_stream(p.other + t * p.ldo + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
+        for (int j0 = 0; j0 < p.topk; j0 += 4) {
+            uint4 v[4][2];
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = j0 + j < p.topk ? row_of(p, t * p.topk + j0 + j) : -1;
+                w[j] = r < 0 ? 0.0f : p.weights ? __ldg(p.weights + t * p.topk + j0 + j) : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[j][i] = r >= 0 && in[i] ? ldg_stream(p.src + r * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float f[8];
+                    unpack8(v[j][i], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(w[j], f[e], acc[i][e]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!in[i]) continue;
+            float f[8];
+            unpack8(res[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[i][e] += f[e];
+            *reinterpret_cast<uint4*>(p.dst + t * p.ldd + c0 + 256 * i) = pack8(acc[i]);
+        }
+    }
+}
+
+// The gradient of combine.  A CTA takes one token: its row of dout is read
+// once, each copy's row of dy is written, each copy's row of y is read for
+// dweights = <dout, y> (8 copies at a time; a thread's binary32 partial sums
+// are added over lanes, then over warps in order).  Further units zero the
+// rows that hold no copy.
+constexpr int kDots = 8;
+
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(MoveParams p) {
+    __shared__ float s_dot[kWarps][kDots];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t zeros = (zero_units(p) + kWarps - 1) / kWarps;
+    const bool dots = p.dweights != nullptr;
+    uint32_t peak = 0;
+    for (int64_t u = blockIdx.x; u < p.tokens + zeros; u += gridDim.x) {
+        if (u >= p.tokens) {
+            const int64_t z = (u - p.tokens) * kWarps + warp;
+            if (z < zero_units(p)) zero_unit(p, z, lane);
+            continue;
+        }
+        for (int j0 = 0; j0 < p.topk; j0 += kDots) {
+            const int64_t copy0 = u * p.topk + j0;
+            const int m = min(kDots, p.topk - j0);
+            int row[kDots];
+            float w[kDots], dot[kDots];
+#pragma unroll
+            for (int j = 0; j < kDots; ++j) {
+                row[j] = j < m ? row_of(p, copy0 + j) : -1;
+                w[j] = j < m && p.weights ? __ldg(p.weights + copy0 + j) : 1.0f;
+                dot[j] = 0.0f;
+            }
+            for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
+                const uint4 g = ldg_stream(p.src + u * p.lds + c);
+                uint4 y[kDots];
+#pragma unroll
+                for (int j = 0; j < kDots; ++j)
+                    if (dots && row[j] >= 0) y[j] = ldg_stream(p.other + row[j] * p.ldo + c);
+                float f[8];
+                unpack8(g, f);
+#pragma unroll
+                for (int j = 0; j < kDots; ++j) {
+                    if (row[j] < 0) continue;
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = w[j] * f[e];
+                    const uint4 d = pack8(o);
+                    peak = absmax8(peak, d);
+                    *reinterpret_cast<uint4*>(p.dst + row[j] * p.ldd + c) = d;
+                    if (dots) {
+                        unpack8(y[j], o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(o[e], f[e], dot[j]);
+                    }
+                }
+            }
+            if (dots) {
+#pragma unroll
+                for (int j = 0; j < kDots; ++j) {
+                    if (j >= m) break;
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+                    if (lane == 0) s_dot[warp][j] = dot[j];
+                }
+                __syncthreads();
+                if (threadIdx.x < m) {
+                    float t = 0.0f;
+                    for (int v = 0; v < kWarps; ++v) t += s_dot[v][threadIdx.x];
+                    p.dweights[copy0 + threadIdx.x] = t;
+                }
+                __syncthreads();
+            }
+        }
+    }
+    if (p.amax) publish_amax(p.amax, peak);
+}
+
+// ----------------------------------------------------------- host side -----
+int sm_count() {
+    static int cached[64];
+    static std::mutex mu;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cached[dev]) {
+        int n = 0;
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        cached[dev] = n > 0 ? n : 148;
+    }
+    return cached[dev];
+}
+
+cudaError_t zero_word(float* amax, cudaStream_t s) {
+    return amax ? cudaMemsetAsync(amax, 0, sizeof(float), s) : cudaSuccess;
+}
+
+MoveParams move_params(const MoveArgs& a) {
+    MoveParams p{};
+    p.src = static_cast<const __nv_bfloat16*>(a.src);
+    p.other = static_cast<const __nv_bfloat16*>(a.other);
+    p.dst = static_cast<__nv_bfloat16*>(a.dst);
+    p.lds = a.lds;
+    p.ldo = a.ldo;
+    p.ldd = a.ldd;
+    p.copy_row = a.copy_row;
+    p.row_copy = a.row_copy;
+    p.weights = a.weights;
+    p.dweights = a.dweights;
+    p.amax = a.amax;
+    p.tokens = a.tokens;
+    p.rows = a.rows;
+    p.cols = a.cols;
+    p.topk = (int)a.topk;
+    return p;
+}
+
+// Enough CTAs for the units, at most 8 (2048 threads) on each SM.
+int grid_for_units(int64_t units) { return (int)std::max<int64_t>(1, std::min<int64_t>(units, (int64_t)sm_count() * 8)); }
+int64_t zero_units_host(const MoveArgs& a) { return ceil_div(a.rows, 32) * ceil_div(a.cols, 1024); }
+
+}  // namespace
+
+cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches) {
+    ActGradParams p{};
+    p.dy = static_cast<const __nv_bfloat16*>(a.dy);
+    p.z = static_cast<const __nv_bfloat16*>(a.z);
+    p.dz = static_cast<__nv_bfloat16*>(a.dz);
+    p.ldy = a.ldy;
+    p.ldz = a.ldz;
+    p.lddz = a.lddz;
+    p.M = a.M;
+    p.N = a.N;
+    p.offsets = a.offsets;
+    p.counts = a.counts;
+    p.experts = (int)a.experts;
+    p.amax = a.amax;
+    const int64_t tiles = ceil_div(a.M, kRowTile);
+    const bool direct = a.dbias && tiles == 1 && !a.offsets;   // one row tile: its sums are the result
+    p.sums = direct ? a.dbias : a.dbias ? a.workspace : nullptr;
+    cudaError_t e = zero_word(a.amax, s);
+    if (e != cudaSuccess) return e;
+    p.strips = ceil_div(a.N, kColTile);
+    const unsigned grid = (unsigned)(tiles * p.strips);
+    switch (a.act) {
+        case ACT_RELU: act_grad_kernel<ACT_RELU><<<grid, kThreads, 0, s>>>(p); break;
+        case ACT_RELU2: act_grad_kernel<ACT_RELU2><<<grid, kThreads, 0, s>>>(p); break;
+        case ACT_GELU: act_grad_kernel<ACT_GELU><<<grid, kThreads, 0, s>>>(p); break;
+        case ACT_GELU_TANH: act_grad_kernel<ACT_GELU_TANH><<<grid, kThreads, 0, s>>>(p); break;
+        case ACT_SILU: act_grad_kernel<ACT_SILU><<<grid, kThreads, 0, s>>>(p); break;
+        default: act_grad_kernel<ACT_NONE><<<grid, kThreads, 0, s>>>(p); break;
+    }
+    *launches += 1;
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.dbias || direct) return e;
+    const dim3 bgrid((unsigned)ceil_div(a.N, 64), (unsigned)(a.offsets ? a.experts : 1));
+    bias_grad_kernel<<<bgrid, kThreads, 0, s>>>(a.workspace, a.M, a.N, a.offsets, a.counts, a.dbias);
+    *launches += 1;
+    return cudaGetLastError();
+}
+
+// CTAs of the sort: about 1024 copies each, fewer where the table of counts
+// that every CTA reads (CTAs x experts) would grow past 64K entries.
+static int64_t sort_ctas(int64_t n, int64_t experts) {
+    return std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 1024), (1 << 16) / experts));
+}
+size_t moe_sort_workspace(int64_t n, int64_t experts) { return (size_t)(sort_ctas(n, experts) * experts * 4); }
+
+cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t s, int* launches) {
+    SortParams p{};
+    p.ids = a.ids;
+    p.n = (int)a.n;
+    p.experts = (int)a.experts;
+    p.rows = (int)a.rows;
+    p.hist = a.workspace;
+    p.offsets = a.offsets;
+    p.counts = a.counts;
+    p.row_copy = a.row_copy;
+    p.copy_row = a.copy_row;
+    p.chunk = (int)(ceil_div(ceil_div(a.n, sort_ctas(a.n, a.experts)), kThreads) * kThreads);
+    const int ctas = (int)ceil_div(a.n, p.chunk);
+    const int smem = (int)(((kWarps + 2) * a.experts + 1) * 4);   // at most 41 KB: 1024 experts
+    if (ctas > 1) {
+        sort_count_kernel<<<ctas, kThreads, p.experts * 4, s>>>(p);
+        *launches += 1;
+    }
+    sort_place_kernel<<<ctas, kThreads, smem, s>>>(p);
+    *launches += 1;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_gather(const MoveArgs& a, cudaStream_t s, int* launches) {
+    cudaError_t e = zero_word(a.amax, s);
+    if (e != cudaSuccess) return e;
+    const int64_t units = a.tokens * ceil_div(a.cols, 1024) + zero_units_host(a);
+    gather_kernel<<<grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s>>>(move_params(a));
+    *launches += 1;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_combine(const MoveArgs& a, cudaStream_t s, int* launches) {
+    const int64_t units = a.tokens * ceil_div(a.cols, 512);
+    combine_kernel<<<grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s>>>(move_params(a));
+    *launches += 1;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_combine_grad(const MoveArgs& a, cudaStream_t s, int* launches) {
+    cudaError_t e = zero_word(a.amax, s);
+    if (e != cudaSuccess) return e;
+    const int64_t units = a.tokens + ceil_div(zero_units_host(a), kWarps);
+    combine_grad_kernel<<<grid_for_units(units), kThreads, 0, s>>>(move_params(a));
+    *launches += 1;
+    return cudaGetLastError();
+}
+
+}  // namespace nvfp4

@@ -27,6 +27,7 @@ NVFP4_OK = 0
 NVFP4_RNE, NVFP4_SR = 0, 1
 NVFP4_SCALE_1D, NVFP4_SCALE_2D = 0, 1
 NVFP4_OUT_F32, NVFP4_OUT_BF16 = 0, 1
+(NVFP4_ACT_NONE, NVFP4_ACT_RELU, NVFP4_ACT_RELU2, NVFP4_ACT_GELU, NVFP4_ACT_GELU_TANH, NVFP4_ACT_SILU) = range(6)
 
 EXPORTS = (
     "nvfp4_version", "nvfp4_status_string", "nvfp4_workspace_size", "nvfp4_mma_scale_bytes",
@@ -34,7 +35,9 @@ EXPORTS = (
     "nvfp4_scales_to_mma", "nvfp4_kernel_launches", "nvfp4_get_error", "nvfp4_quantize_1d_noalloc",
     "nvfp4_selftest_wait_timeout", "nvfp4_quantize_1d_from_amax", "nvfp4_quantize_2d_from_amax",
     "nvfp4_gemm_amax", "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_dequantize", "nvfp4_mxfp4_gemm",
-    "nvfp4_quantize_dual", "nvfp4_rht_quantize_n",
+    "nvfp4_quantize_dual", "nvfp4_rht_quantize_n", "nvfp4_gemm_epilogue", "nvfp4_act_grad_workspace_size",
+    "nvfp4_act_grad", "nvfp4_moe_rows", "nvfp4_moe_workspace_size", "nvfp4_moe_sort", "nvfp4_moe_gather",
+    "nvfp4_moe_combine", "nvfp4_moe_combine_grad", "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_wgrad",
 )
 
 _lib = None
@@ -100,6 +103,30 @@ def lib():
                                           sz, vp]
         L.nvfp4_mxfp4_gemm.restype = ci
         L.nvfp4_mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, vp, i64, vp]
+        L.nvfp4_gemm_epilogue.restype = ci
+        L.nvfp4_gemm_epilogue.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, ci, vp, i64, ci, vp, i64, vp, i64,
+                                          vp, vp]
+        L.nvfp4_act_grad_workspace_size.restype = sz
+        L.nvfp4_act_grad_workspace_size.argtypes = [i64, i64]
+        L.nvfp4_act_grad.restype = ci
+        L.nvfp4_act_grad.argtypes = [vp, i64, vp, i64, i64, i64, ci, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+        L.nvfp4_moe_rows.restype = i64
+        L.nvfp4_moe_rows.argtypes = [i64, i64]
+        L.nvfp4_moe_workspace_size.restype = sz
+        L.nvfp4_moe_workspace_size.argtypes = [i64, i64]
+        L.nvfp4_moe_sort.restype = ci
+        L.nvfp4_moe_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]
+        L.nvfp4_moe_gather.restype = ci
+        L.nvfp4_moe_gather.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp, vp]
+        L.nvfp4_moe_combine.restype = ci
+        L.nvfp4_moe_combine.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+        L.nvfp4_moe_combine_grad.restype = ci
+        L.nvfp4_moe_combine_grad.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp, vp]
+        L.nvfp4_gemm_grouped.restype = ci
+        L.nvfp4_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, ci, vp, i64, ci, vp,
+                                         i64, vp, i64, vp, vp]
+        L.nvfp4_gemm_grouped_wgrad.restype = ci
+        L.nvfp4_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -244,6 +271,72 @@ def nvfp4_mxfp4_gemm(a_codes, a_scales_mma, b_codes, b_scales_mma, M, N, K, out_
 def nvfp4_scales_to_mma(scales, scale_mode, rows, k, scales_mma, stream=None):
     _check("nvfp4_scales_to_mma", lib().nvfp4_scales_to_mma(
         _p(scales), scale_mode, rows, k, _p(scales_mma), _stream(stream)))
+
+
+def nvfp4_gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation, residual,
+                        ldr, out_dtype, c, ldc, pre, ldp, c_amax, stream=None):
+    _check("nvfp4_gemm_epilogue", lib().nvfp4_gemm_epilogue(
+        _p(a_codes), _p(a_scales_mma), _p(a_gs), _p(b_codes), _p(b_scales_mma), _p(b_gs), M, N, K, _p(bias),
+        activation, _p(residual), ldr, out_dtype, _p(c), ldc, _p(pre), ldp, _p(c_amax), _stream(stream)))
+
+
+def nvfp4_act_grad_workspace_size(M: int, N: int) -> int:
+    return lib().nvfp4_act_grad_workspace_size(M, N)
+
+
+def nvfp4_act_grad(dy, ldy, z, ldz, M, N, activation, offsets, counts, experts, dz, lddz, dbias, amax, workspace,
+                   ws_bytes, stream=None):
+    _check("nvfp4_act_grad", lib().nvfp4_act_grad(
+        _p(dy), ldy, _p(z), ldz, M, N, activation, _p(offsets), _p(counts), experts, _p(dz), lddz, _p(dbias),
+        _p(amax), _p(workspace), ws_bytes, _stream(stream)))
+
+
+def nvfp4_moe_rows(copies: int, experts: int) -> int:
+    return lib().nvfp4_moe_rows(copies, experts)
+
+
+def nvfp4_moe_workspace_size(copies: int, experts: int) -> int:
+    return lib().nvfp4_moe_workspace_size(copies, experts)
+
+
+def nvfp4_moe_sort(expert_ids, copies, experts, rows, offsets, counts, row_copy, copy_row, workspace, ws_bytes,
+                   stream=None):
+    _check("nvfp4_moe_sort", lib().nvfp4_moe_sort(
+        _p(expert_ids), copies, experts, rows, _p(offsets), _p(counts), _p(row_copy), _p(copy_row), _p(workspace),
+        ws_bytes, _stream(stream)))
+
+
+def nvfp4_moe_gather(x, ldx, tokens, topk, cols, copy_row, row_copy, rows, y, ldy, amax, stream=None):
+    _check("nvfp4_moe_gather", lib().nvfp4_moe_gather(
+        _p(x), ldx, tokens, topk, cols, _p(copy_row), _p(row_copy), rows, _p(y), ldy, _p(amax), _stream(stream)))
+
+
+def nvfp4_moe_combine(y, ldy, rows, cols, copy_row, weights, residual, ldr, tokens, topk, out, ldo, stream=None):
+    _check("nvfp4_moe_combine", lib().nvfp4_moe_combine(
+        _p(y), ldy, rows, cols, _p(copy_row), _p(weights), _p(residual), ldr, tokens, topk, _p(out), ldo,
+        _stream(stream)))
+
+
+def nvfp4_moe_combine_grad(dout, ldo, y, ldy, tokens, topk, cols, copy_row, row_copy, rows, weights, dy, lddy,
+                           dweights, amax, stream=None):
+    _check("nvfp4_moe_combine_grad", lib().nvfp4_moe_combine_grad(
+        _p(dout), ldo, _p(y), ldy, tokens, topk, cols, _p(copy_row), _p(row_copy), rows, _p(weights), _p(dy), lddy,
+        _p(dweights), _p(amax), _stream(stream)))
+
+
+def nvfp4_gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, offsets, counts, experts, M, N, K,
+                       bias, activation, residual, ldr, out_dtype, c, ldc, pre, ldp, c_amax, stream=None):
+    _check("nvfp4_gemm_grouped", lib().nvfp4_gemm_grouped(
+        _p(a_codes), _p(a_scales_mma), _p(a_gs), _p(b_codes), _p(b_scales_mma), _p(b_gs), _p(offsets), _p(counts),
+        experts, M, N, K, _p(bias), activation, _p(residual), ldr, out_dtype, _p(c), ldc, _p(pre), ldp, _p(c_amax),
+        _stream(stream)))
+
+
+def nvfp4_gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, offsets, counts, experts, M,
+                             N, K, out_dtype, c, ldc, stream=None):
+    _check("nvfp4_gemm_grouped_wgrad", lib().nvfp4_gemm_grouped_wgrad(
+        _p(a_codes), _p(a_scales_mma), _p(a_gs), _p(b_codes), _p(b_scales_mma), _p(b_gs), _p(offsets), _p(counts),
+        experts, M, N, K, out_dtype, _p(c), ldc, _stream(stream)))
 
 
 def nvfp4_get_error(stream=None) -> int:
@@ -405,3 +498,245 @@ def quantize_dual(x: torch.Tensor, rounding: int = NVFP4_RNE, sr_seed: int = 0, 
                         q1.global_scale, rht_seed, sr_seed_t, q2.codes, q2.scales, q2.scales_mma, q2.global_scale,
                         ws, ws.numel(), stream)
     return q1, q2
+
+
+# ------------------------------------------------------ the linear layer ----
+def _matrix(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> int:
+    """Row stride of a [rows x cols] matrix with unit column stride (checked)."""
+    assert t.dtype == dtype and t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1)
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _padded(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A [rows x cols] view whose row stride is a multiple of 8 elements."""
+    ld = (cols + 7) // 8 * 8
+    t = torch.empty(rows, ld, dtype=dtype, device=device)
+    return t if ld == cols else t[:, :cols]
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Device scratch of one call: not reused before that call's stream is past it."""
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
+    assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.numel() == experts * rows * (k // 2)
+    assert scales_mma.is_contiguous() and scales_mma.numel() >= experts * nvfp4_mma_scale_bytes(rows, k)
+    assert gs.dtype == torch.float32 and gs.is_contiguous() and gs.numel() == experts
+
+
+def _check_word(t):
+    assert t is None or (t.dtype == torch.float32 and t.numel() == 1)
+
+
+def gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: int, K: int, bias=None,
+                  activation: int = NVFP4_ACT_NONE, residual: Optional[torch.Tensor] = None,
+                  out_dtype: int = NVFP4_OUT_BF16, out: Optional[torch.Tensor] = None,
+                  pre: Optional[torch.Tensor] = None, amax_out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """C = act(alpha * A . B^T + bias) + residual with NVFP4 operands (MMA-layout scales).
+
+    bias bf16 [N]; residual bf16 [M x N], which may be `out`; `pre` (bf16 [M x N]) receives the
+    pre-activation and `amax_out` (a device float) max |C|."""
+    _check_operand(a_codes, a_scales_mma, a_gs, M, K)
+    _check_operand(b_codes, b_scales_mma, b_gs, N, K)
+    return _gemm_layer(None, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation,
+                       residual, out_dtype, out, pre, amax_out, stream)
+
+
+def _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation, residual,
+                out_dtype, out, pre, amax_out, stream):
+    experts = 1 if plan is None else plan.experts
+    if bias is not None:
+        assert bias.dtype == torch.bfloat16 and bias.is_contiguous() and bias.numel() == experts * N
+    _check_word(amax_out)
+    dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
+    if out is None:
+        out = _padded(M, N, dt, a_codes.device)
+    ldc = _matrix(out, M, N, dt)
+    ldr = _matrix(residual, M, N) if residual is not None else 0
+    ldp = _matrix(pre, M, N) if pre is not None else 0
+    if plan is None:
+        nvfp4_gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation,
+                            residual, ldr, out_dtype, out, ldc, pre, ldp, amax_out, stream)
+    else:
+        nvfp4_gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan.offsets, plan.counts,
+                           experts, M, N, K, bias, activation, residual, ldr, out_dtype, out, ldc, pre, ldp,
+                           amax_out, stream)
+    return out
+
+
+def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_grad: bool = True,
+             plan: "Optional[MoePlan]" = None, out: Optional[torch.Tensor] = None,
+             amax_out: Optional[torch.Tensor] = None, stream=None):
+    """(dz, dbias) of C = act(z) + residual with z = product + bias: dz = dy * act'(z) in bf16, dbias its column
+    sums in fp32 ([N], with a plan [experts x N]; None without bias_grad).  z is the `pre` of gemm_epilogue."""
+    M, N = dy.shape
+    ldy = _matrix(dy, M, N)
+    ldz = _matrix(z, M, N) if z is not None else 0
+    if out is None:
+        out = _padded(M, N, torch.bfloat16, dy.device)
+    lddz = _matrix(out, M, N)
+    _check_word(amax_out)
+    dbias = ws = None
+    experts = 0 if plan is None else plan.experts
+    assert plan is None or plan.rows == M
+    if bias_grad:
+        dbias = torch.empty((experts, N) if experts else (N,), dtype=torch.float32, device=dy.device)
+        ws = _scratch(nvfp4_act_grad_workspace_size(M, N), dy.device, stream)
+    nvfp4_act_grad(dy, ldy, z, ldz, M, N, activation, plan.offsets if experts else None,
+                   plan.counts if experts else None, experts, out, lddz, dbias, amax_out, ws,
+                   ws.numel() if bias_grad else 0, stream)
+    return out, dbias
+
+
+# --------------------------------------------------- the layer of experts ---
+@dataclass
+class MoePlan:
+    """Where the copies of routed tokens go: rows sorted by expert (int32 device tensors, see nvfp4_moe_sort)."""
+    offsets: torch.Tensor    # [experts + 1]
+    counts: torch.Tensor     # [experts]
+    row_copy: torch.Tensor   # [rows]
+    copy_row: torch.Tensor   # [tokens, topk]
+
+    def __post_init__(self):
+        for t in (self.offsets, self.counts, self.row_copy, self.copy_row):
+            assert t.dtype == torch.int32 and t.is_contiguous()
+        assert self.offsets.numel() == self.counts.numel() + 1 and self.copy_row.dim() == 2
+
+    @property
+    def experts(self) -> int:
+        return self.counts.numel()
+
+    @property
+    def rows(self) -> int:
+        return self.row_copy.numel()
+
+    @property
+    def tokens(self) -> int:
+        return self.copy_row.shape[0]
+
+    @property
+    def topk(self) -> int:
+        return self.copy_row.shape[1]
+
+
+def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None, stream=None) -> MoePlan:
+    """Sort the copies of int32 expert_ids [tokens x topk] by expert.  rows (default: enough for every routing)
+    bounds the sorted matrices; copies that find no row are dropped."""
+    assert expert_ids.dtype == torch.int32 and expert_ids.dim() == 2 and expert_ids.is_contiguous()
+    n, dev = expert_ids.numel(), expert_ids.device
+    if rows is None:
+        rows = nvfp4_moe_rows(n, experts)
+    plan = MoePlan(torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                   torch.empty(experts, dtype=torch.int32, device=dev),
+                   torch.empty(rows, dtype=torch.int32, device=dev),
+                   torch.empty(expert_ids.shape, dtype=torch.int32, device=dev))
+    ws = _scratch(nvfp4_moe_workspace_size(n, experts), dev, stream)
+    nvfp4_moe_sort(expert_ids, n, experts, rows, plan.offsets, plan.counts, plan.row_copy, plan.copy_row, ws,
+                   ws.numel(), stream)
+    return plan
+
+
+def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = None,
+               amax_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The token rows x bf16 [tokens x cols] sorted by expert: bf16 [rows x cols], zeros in padding rows.  With
+    `amax_out` (a device float) also max |x|, for the quantizers.  Its gradient is moe_combine without weights."""
+    cols = x.shape[1]
+    if out is None:
+        out = torch.empty(plan.rows, cols, dtype=torch.bfloat16, device=x.device)
+    _check_word(amax_out)
+    nvfp4_moe_gather(x, _matrix(x, plan.tokens, cols), plan.tokens, plan.topk, cols, plan.copy_row, plan.row_copy,
+                     plan.rows, out, _matrix(out, plan.rows, cols), amax_out, stream)
+    return out
+
+
+def _check_weights(weights, plan):
+    assert weights is None or (weights.dtype == torch.float32 and weights.is_contiguous()
+                               and weights.shape == plan.copy_row.shape)
+
+
+def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """residual[t] + sum_j weights[t, j] * y[row of copy (t, j)]: bf16 [tokens x cols]; weights fp32 or None (1)."""
+    cols = y.shape[1]
+    _check_weights(weights, plan)
+    if out is None:
+        out = torch.empty(plan.tokens, cols, dtype=torch.bfloat16, device=y.device)
+    nvfp4_moe_combine(y, _matrix(y, plan.rows, cols), plan.rows, cols, plan.copy_row, weights, residual,
+                      _matrix(residual, plan.tokens, cols) if residual is not None else 0, plan.tokens, plan.topk,
+                      out, _matrix(out, plan.tokens, cols), stream)
+    return out
+
+
+def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], plan: MoePlan,
+                     weights: Optional[torch.Tensor] = None, amax_out: Optional[torch.Tensor] = None, stream=None):
+    """(dy, dweights) of moe_combine: dy bf16 [rows x cols] with zeros in padding rows, dweights fp32
+    [tokens x topk] (None when y is None)."""
+    cols = dout.shape[1]
+    _check_weights(weights, plan)
+    _check_word(amax_out)
+    dy = torch.empty(plan.rows, cols, dtype=torch.bfloat16, device=dout.device)
+    dw = torch.empty(plan.copy_row.shape, dtype=torch.float32, device=dout.device) if y is not None else None
+    nvfp4_moe_combine_grad(dout, _matrix(dout, plan.tokens, cols), y,
+                           _matrix(y, plan.rows, cols) if y is not None else 0, plan.tokens, plan.topk, cols,
+                           plan.copy_row, plan.row_copy, plan.rows, weights, dy, cols, dw, amax_out, stream)
+    return dy, dw
+
+
+def gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan: MoePlan, M: int, N: int, K: int,
+                 bias=None, activation: int = NVFP4_ACT_NONE, residual: Optional[torch.Tensor] = None,
+                 out_dtype: int = NVFP4_OUT_BF16, out: Optional[torch.Tensor] = None,
+                 pre: Optional[torch.Tensor] = None, amax_out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """gemm_epilogue over M rows sorted by expert: b_codes [experts x N x K/2], their scales and b_gs [experts],
+    bias [experts x N].  Padding rows of C (and pre) are zeros."""
+    assert plan.rows == M
+    _check_operand(a_codes, a_scales_mma, a_gs, M, K)
+    _check_operand(b_codes, b_scales_mma, b_gs, N, K, plan.experts)
+    return _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation,
+                       residual, out_dtype, out, pre, amax_out, stream)
+
+
+def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan: MoePlan, M: int, N: int,
+                       K: int, out_dtype: int = NVFP4_OUT_F32, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """[experts x M x N]: per expert A . B^T over its K sorted rows, A [M x K] and B [N x K] the transposed
+    operands."""
+    assert plan.rows == K
+    _check_operand(a_codes, a_scales_mma, a_gs, M, K)
+    _check_operand(b_codes, b_scales_mma, b_gs, N, K)
+    dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
+    if out is None:
+        out = _padded(plan.experts * M, N, dt, a_codes.device).unflatten(0, (plan.experts, M))
+    assert out.dtype == dt and out.shape == (plan.experts, M, N) and out.stride(2) == 1
+    assert plan.experts == 1 or out.stride(0) == M * out.stride(1)
+    nvfp4_gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan.offsets, plan.counts,
+                             plan.experts, M, N, K, out_dtype, out, out.stride(1), stream)
+    return out
+
+
+def quantize_2d_experts(w: torch.Tensor, columnwise: bool = True, stream=None):
+    """(W, W^T) operands of gemm_grouped from expert weights bf16 [experts x rows x cols], each quantized by
+    quantize_2d: Quantized with stacked codes, scales and global scales (the second None without columnwise)."""
+    assert w.dtype == torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1
+    experts, rows, cols = w.shape
+    dev = w.device
+    row = Quantized(torch.empty(experts, rows, cols // 2, dtype=torch.uint8, device=dev), None,
+                    torch.empty(experts, nvfp4_mma_scale_bytes(rows, cols), dtype=torch.uint8, device=dev),
+                    torch.empty(experts, dtype=torch.float32, device=dev), rows, cols)
+    col = Quantized(torch.empty(experts, cols, rows // 2, dtype=torch.uint8, device=dev), None,
+                    torch.empty(experts, nvfp4_mma_scale_bytes(cols, rows), dtype=torch.uint8, device=dev),
+                    row.global_scale, cols, rows) if columnwise else None
+    ws = _scratch(nvfp4_workspace_size(rows, cols), dev, stream)
+    for e in range(experts):
+        nvfp4_quantize_2d(w[e], rows, cols, w.stride(1), row.codes[e], col.codes[e] if columnwise else None, None,
+                          row.scales_mma[e], col.scales_mma[e] if columnwise else None, row.global_scale[e:e + 1],
+                          ws, ws.numel(), stream)
+    return row, col
