@@ -414,7 +414,7 @@ nvfp4_status nvfp4_act_grad(const void* dy, int64_t ldy, const void* z, int64_t 
  *   row_copy   int32 [rows]: the row's copy, -1 for padding.
  *   copy_row   int32 [copies]: the copy's row, -1 if dropped.
  *   Workspace: >= nvfp4_moe_workspace_size(copies, experts), 16-byte aligned.
- *   experts in [1, 1024].
+ *   experts in [1, 512].
  * The calls below take these arrays as device data; values that no sort would
  * give are not followed out of bounds, but the results are then unspecified. */
 int64_t nvfp4_moe_rows(int64_t copies, int64_t experts);
@@ -451,7 +451,7 @@ nvfp4_status nvfp4_moe_combine_grad(const void* dout, int64_t ldo, const void* y
 
 /* The experts' products: nvfp4_gemm_epilogue over sorted rows, rows of expert e
  * with weight e.  A [M rows] as quantized from sorted rows (M a multiple of
- * 128); b_codes [experts x N x K/2], b_scales_mma experts x
+ * 128, at most 2^23); b_codes [experts x N x K/2], b_scales_mma experts x
  * nvfp4_mma_scale_bytes(N, K) bytes, b_gs [experts]; bias [experts x N].
  * Padding rows of C and pre become zeros (the residual is not added there),
  * whatever A holds in them.  With the codes of the transposed weights this is

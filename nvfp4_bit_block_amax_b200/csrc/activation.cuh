@@ -7,9 +7,10 @@
 //   gelu_tanh  z s(2 u), u = sqrt(2/pi) (z + 0.044715 z^3), which is
 //              z (1 + tanh u) / 2: one exponential instead of a tanh
 //              slope  s + z s (1 - s) 2 u'
-// The logistic uses the fast exponential and division (each good to a few
-// binary32 steps, 2^-21 relative): far below the bf16 step of the results and
-// the same order as the rounding of the sums they are applied to.
+// The logistic uses the hardware's exponential and reciprocal (each good to two
+// binary32 steps, together below 2^-21 relative): far below the bf16 step of
+// the results and the same order as the rounding of the sums they are applied
+// to.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,10 +20,45 @@ namespace nvfp4 {
 enum Activation { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU2 = 2, ACT_GELU = 3, ACT_GELU_TANH = 4, ACT_SILU = 5 };
 constexpr int kNumActivations = 6;
 
+// 2^x and 1/x, the hardware's approximations (2 and 1 units in the last place)
+// with subnormals as zeros: one instruction each, where exp and the division
+// with subnormals kept take four or five.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 // exp(-x) overflows to infinity below x = -88, where the quotient is 0.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
-// __fdividef(1, y) is 0 for y in (2^126, 2^128) and for infinite y: the true
-// quotient is below 2^-126 there.
+__device__ __forceinline__ float logistic(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }
+
+// The normal distribution function and its density, by Hastings' polynomial
+// for the error function (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26): with x = |z| / sqrt(2) and t = 1 / (1 + 0.3275911 x),
+// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) to 1.5e-7, and the error falls off
+// with exp(-x^2) like the function, so that P(-|z|) = erfc(x) / 2 is good far
+// out too.  One exponential and one division serve both results; the library's
+// normcdff takes three times the instructions.
+constexpr float kHastingsP = 0.3275911f * 0.70710678f;   // of |z|, not of x
+constexpr float kHastings1 = 0.254829592f, kHastings2 = -0.284496736f, kHastings3 = 1.421413741f,
+                kHastings4 = -1.453152027f, kHastings5 = 1.061405429f;
+struct Normal {
+    float cdf, pdf;
+};
+__device__ __forceinline__ Normal normal(float z) {
+    const float e = exp2_fast(-0.5f * kLog2e * z * z);
+    const float t = rcp_fast(fmaf(kHastingsP, fabsf(z), 1.0f));
+    const float poly =
+        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, kHastings5, kHastings4), kHastings3), kHastings2), kHastings1);
+    const float tail = 0.5f * poly * e;
+    return Normal{z > 0.0f ? 1.0f - tail : tail, 0.3989422804f * e};
+}
 
 constexpr float kTanhScale2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
@@ -34,7 +70,7 @@ __device__ __forceinline__ float act_value(float z) {
         const float r = fmaxf(z, 0.0f);
         return r * r;
     }
-    if constexpr (ACT == ACT_GELU) return z * normcdff(z);
+    if constexpr (ACT == ACT_GELU) return z * normal(z).cdf;
     if constexpr (ACT == ACT_GELU_TANH) return z * logistic(kTanhScale2 * z * fmaf(kTanhCubic * z, z, 1.0f));
     if constexpr (ACT == ACT_SILU) return z * logistic(z);
     return z;
@@ -43,7 +79,10 @@ __device__ __forceinline__ float act_value(float z) {
 template <int ACT>   // not for NONE and RELU2, see act_grad_value
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (ACT == ACT_GELU) return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), normcdff(z));
+    if constexpr (ACT == ACT_GELU) {
+        const Normal n = normal(z);
+        return n.pdf == 0.0f ? n.cdf : fmaf(z, n.pdf, n.cdf);   // 0 far out, where z may be anything
+    }
     if constexpr (ACT == ACT_GELU_TANH) {
         const float zz = z * z;
         const float s = logistic(kTanhScale2 * z * fmaf(kTanhCubic, zz, 1.0f));
@@ -65,33 +104,32 @@ __device__ __forceinline__ float act_grad_value(float g, float z) {
     else return g * act_slope<ACT>(z);
 }
 
-// The activation applied to n values; the choice is uniform over the grid, so
-// it is made once per group of values and not once per value.
-template <int N>
-__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
-    switch (act) {
-        case ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<ACT_RELU>(v[i]);
-            break;
-        case ACT_RELU2:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<ACT_RELU2>(v[i]);
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<ACT_GELU>(v[i]);
-            break;
-        case ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<ACT_GELU_TANH>(v[i]);
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<ACT_SILU>(v[i]);
-            break;
-        default: break;
-    }
+// The activation of two values at once, through the two-wide multiply and add
+// where the formula is made of them.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 logistic2(float2 x_log2e_neg) {   // of -x log2(e)
+    const float2 d = __fadd2_rn(make_float2(exp2_fast(x_log2e_neg.x), exp2_fast(x_log2e_neg.y)), both(1.0f));
+    return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+}
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 z) {
+    if constexpr (ACT == ACT_SILU) return __fmul2_rn(z, logistic2(__fmul2_rn(z, both(-kLog2e))));
+    else if constexpr (ACT == ACT_GELU_TANH) {
+        const float2 zz = __fmul2_rn(z, z);
+        const float2 u = __ffma2_rn(zz, both(-kLog2e * kTanhScale2 * kTanhCubic), both(-kLog2e * kTanhScale2));
+        return __fmul2_rn(z, logistic2(__fmul2_rn(z, u)));
+    } else if constexpr (ACT == ACT_GELU) {
+        const float2 q = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
+        const float2 d = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(kHastingsP), both(1.0f));
+        const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+        float2 poly = __ffma2_rn(t, both(0.5f * kHastings5), both(0.5f * kHastings4));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings3));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings2));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings1));
+        // z P(z) = max(z, 0) - |z| P(-|z|)
+        const float2 tail = __fmul2_rn(__fmul2_rn(t, poly), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
+        return make_float2(fmaf(-fabsf(z.x), tail.x, fmaxf(z.x, 0.0f)), fmaf(-fabsf(z.y), tail.y, fmaxf(z.y, 0.0f)));
+    } else return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
 }
 
 }  // namespace nvfp4

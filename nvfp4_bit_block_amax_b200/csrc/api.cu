@@ -380,6 +380,7 @@ static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
     if (g.experts && (!g.offsets || !g.counts || g.experts < 1 || g.experts > kMaxExpertsArg ||
                       g.experts * g.N >= kMaxDim || g.experts * g.M >= kMaxDim * 128))
         return NVFP4_ERR_INVALID_ARG;
+    if (g.experts && !g.wgrad && g.M > kMaxSortedRows) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (g.K % 64 || (g.experts && (g.wgrad ? g.K : g.M) % 128)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(g.a) || !aligned16(g.b) || !aligned16(g.sfa) || !aligned16(g.sfb) || !aligned16(g.c) || g.ldc % 8 ||
         !aligned4(g.a_gs) || !aligned4(g.b_gs) || !aligned2(g.bias) || !aligned4(g.c_amax) || !aligned4(g.offsets) ||

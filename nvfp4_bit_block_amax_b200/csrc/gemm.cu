@@ -98,7 +98,6 @@ struct KParams {
     const __nv_bfloat16* bias;      // [experts x N] or nullptr
     const __nv_bfloat16* residual;  // [M x ldr] or nullptr
     int64_t ldr;
-    int act;
     __nv_bfloat16* pre;             // [M x ldp] or nullptr: also store the pre-activation
     int64_t ldp;
     const int* offsets;             // [experts + 1] first row (or K index) of each expert's segment
@@ -114,7 +113,7 @@ struct KParams {
 //             rows that belong to no token become zeros
 //   KSEG      one product per expert, C_e = alpha A . B^T over K in e's segment
 enum Mode { PLAIN, EPILOGUE, ROWS, KSEG };
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = 512;
 
 // Fold this thread's maximum |C| (binary32 bits, non-negative) into c_amax:
 // one atomic per warp, once per kernel (the epilogue roles keep a running
@@ -529,21 +528,29 @@ constexpr int P_OFF_MISC = P_OFF_BAR + P_NUM_BARS * 8;
 constexpr int P_OFF_EPI = (P_OFF_MISC + 16 + 1023) / 1024 * 1024;   // output staging, one 2 KB buffer per epilogue warp
 constexpr int EPI_BUF = 2048;                                      // 32 rows x 64 bytes, 64-byte swizzle
 constexpr int P_SMEM_BYTES = P_OFF_EPI + 8 * EPI_BUF + 1024;
-// The modes beyond PLAIN keep, behind that, one expert table (see Groups) and
-// the bias of each epilogue warp's 128 columns.
-constexpr int X_OFF_BIAS = P_OFF_EPI + 8 * EPI_BUF;
-constexpr int X_OFF_GROUPS = X_OFF_BIAS + 8 * 128 * 4;
-constexpr int X_SMEM_BYTES = X_OFF_GROUPS + (3 * kMaxExperts + 4) * 4 + 1024;
+// The modes beyond PLAIN have 4 KB of staging per epilogue warp, the bias of
+// its 128 columns, and an expert table (see Groups).
+constexpr int X_EPI_BUF = 32 * 128;
+constexpr int X_OFF_EPI = (P_OFF_MISC + 16 + 127) / 128 * 128;
+constexpr int X_OFF_BIAS = X_OFF_EPI + 8 * X_EPI_BUF;
+constexpr int X_OFF_GROUPS = X_OFF_BIAS + 8 * 256;
+constexpr int X_SMEM_BYTES = X_OFF_GROUPS + (kMaxExperts + 2) * 2 + 1024;
 static_assert(X_SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 constexpr int P_NUM_THREADS = 448;                  // 14 warps: producer, MMA, 4 scale warps, 8 epilogue warps
+// The modes beyond PLAIN: 16 warps in 4 warpgroups, so that registers can be
+// moved between them (setmaxnreg): producer, MMA and two idle warps; the scale
+// warps; two of epilogue warps, which hold their 128 columns in registers
+// while they work on them.  512 threads start with 128 registers each:
+// 256 x 72 + 256 x 184 = 65536.
+constexpr int X_NUM_THREADS = 512;
+constexpr int X_REGS_OTHERS = 72, X_REGS_EPILOGUE = 184;
+static_assert(256 * X_REGS_OTHERS + 256 * X_REGS_EPILOGUE <= X_NUM_THREADS * 128, "registers of the CTA at launch");
 // M = 256 (pair), N = 256, E2M1 x E2M1, UE4M3 scales, K-major.
 constexpr uint32_t kIdescPair = (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 
 // Stage one 32-row x 64-byte chunk (this lane's row: 16 words) and store it.
-// PLANES: C is a stack of matrices, the third coordinate says which.
-template <bool PLANES = false>
 __device__ __forceinline__ void store_chunk(const CUtensorMap* map_c, uint32_t buf, int lane, const uint32_t* w, int col,
-                                            int row0, int plane, bool first) {
+                                            int row0, bool first) {
     if (!first) {
         if (lane == 0) bulk_wait_read0();   // the buffer's previous chunk has been read out
         __syncwarp();
@@ -555,8 +562,7 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map_c, uint32_t b
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        if constexpr (PLANES) tma_store_3d(map_c, buf, col, row0, plane);
-        else tma_store_2d(map_c, buf, col, row0);
+        tma_store_2d(map_c, buf, col, row0);
         bulk_commit();
     }
 }
@@ -606,7 +612,7 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
         if (row0 < p.M && ncols > 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (32 * k < ncols) store_chunk(map_c, buf, lane, packed + 16 * k, col0 + 32 * k, row0, 0, first);
+                if (32 * k < ncols) store_chunk(map_c, buf, lane, packed + 16 * k, col0 + 32 * k, row0, first);
                 first = false;
             }
         }
@@ -635,7 +641,7 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
             if (live) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (32 * i + 16 * h < ncols) store_chunk(map_c, buf, lane, f + 16 * h, col0 + 32 * i + 16 * h, row0, 0, first);
+                    if (32 * i + 16 * h < ncols) store_chunk(map_c, buf, lane, f + 16 * h, col0 + 32 * i + 16 * h, row0, first);
                     first = false;
                 }
             }
@@ -646,54 +652,44 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
 }
 
 // ------------------------------------------------- tiles of the pair kernel --
-// Expert segments in shared memory.  offsets and counts are device data that
-// nothing has checked: here they are clamped so that every segment is a
-// non-decreasing 128-aligned range inside [0, limit) and holds its count, and
-// whatever they were, no tile leaves the operands.
+// Expert segments.  offsets and counts are device data that nothing has
+// checked: wherever they are read they are clamped to 128-aligned ranges inside
+// [0, limit), and a tile whose rows would leave the operands is left out, so
+// that whatever they held, no access goes out of bounds.  ROWS also needs to
+// know which segment an M-tile lies in: a table in shared memory holds the
+// first M-tile of each expert, its last entry the number of M-tiles; the rows
+// behind the last segment are a segment of their own, without an expert.
 struct Groups {
-    int* first;   // [experts + 2] ROWS: first M-tile of each expert; entry `experts` is the rows behind the last one
-    int* start;   // [experts + 1]
-    int* end;     // [experts]     start + count
+    uint16_t* first;   // [experts + 2]
 };
 __device__ __forceinline__ Groups groups_at(uint8_t* smem) {
-    int* base = reinterpret_cast<int*>(smem + X_OFF_GROUPS);
-    return Groups{base, base + kMaxExperts + 2, base + 2 * kMaxExperts + 3};
+    return Groups{reinterpret_cast<uint16_t*>(smem + X_OFF_GROUPS)};
 }
-// One warp fills the table (running maximum and running sum over lanes).
-__device__ __forceinline__ void fill_groups(const Groups& g, const KParams& p, int limit, int lane) {
+__device__ __forceinline__ int segment_start(const KParams& p, int e, int limit) {
+    return min(max(__ldg(p.offsets + e), 0), limit) & ~127;
+}
+__device__ __forceinline__ int segment_end(const KParams& p, int e, int limit) {
+    const int start = segment_start(p, e, limit);
+    return start + min(max(__ldg(p.counts + e), 0), max(segment_start(p, e + 1, limit) - start, 0));
+}
+// One warp fills the table (a running sum over lanes).
+__device__ __forceinline__ void fill_groups(const Groups& g, const KParams& p, int lane) {
     int carry = 0;
-    for (int base = 0; base <= p.experts; base += 32) {
-        const int i = base + lane;
-        int v = i <= p.experts ? min(max(__ldg(p.offsets + i), 0), limit) & ~127 : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-            if (lane >= d) v = max(v, u);
-        }
-        v = max(v, carry);
-        if (i <= p.experts) g.start[i] = v;
-        carry = __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-    __syncwarp();
-    carry = 0;
     if (lane == 0) g.first[0] = 0;
     for (int base = 0; base <= p.experts; base += 32) {
         const int i = base + lane;
         int n = 0;
-        if (i < p.experts) {
-            const int len = g.start[i + 1] - g.start[i];
-            g.end[i] = g.start[i] + min(max(__ldg(p.counts + i), 0), len);
-            n = (len + 255) >> 8;
-        } else if (i == p.experts) {
-            n = (limit - g.start[i] + 255) >> 8;
+        if (i <= p.experts) {
+            const int end = i < p.experts ? segment_start(p, i + 1, p.M) : p.M;
+            n = (max(end - segment_start(p, i, p.M), 0) + 255) >> 8;
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, n, d);
             if (lane >= d) n += u;
         }
-        n += carry;
-        if (i <= p.experts) g.first[i + 1] = n;
+        n = min(n + carry, 65535);   // a sort's segments give fewer: M is at most 2^23 (see nvfp4.h)
+        if (i <= p.experts) g.first[i + 1] = (uint16_t)n;
         carry = __shfl_sync(0xFFFFFFFFu, n, 31);
     }
 }
@@ -726,23 +722,25 @@ __device__ __forceinline__ Tile tile_at(int t, const KParams& p, const Groups& g
             else hi = mid - 1;
         }
         r.e = lo;
-        r.m0 = g.start[lo] + (tm - g.first[lo]) * 256;
+        r.m0 = segment_start(p, lo, p.M) + (tm - g.first[lo]) * 256;
         r.k0 = 0;
         if (lo < p.experts) {
-            r.row_end = g.start[lo + 1];
-            r.row_live = g.end[lo];
+            r.row_end = segment_start(p, lo + 1, p.M);
+            r.row_live = segment_end(p, lo, p.M);
         } else {                      // behind the last segment
             r.row_end = p.M;
             r.row_live = 0;
         }
         r.k_steps = r.m0 < r.row_live ? p.K / 64 : 0;
+        if (r.m0 >= r.row_end) r.row_end = r.k_steps = 0;   // not from a sort's offsets
     } else if constexpr (MODE == KSEG) {
         const int per = p.tiles_m * p.tiles_n;
         r.e = t / per;
         tile_coords(t - r.e * per, p, tm, tn);
         r.m0 = tm * 256;
-        r.k0 = g.start[r.e] >> 6;
-        r.k_steps = (g.end[r.e] - g.start[r.e] + 63) >> 6;
+        const int start = segment_start(p, r.e, p.K);
+        r.k0 = start >> 6;
+        r.k_steps = (segment_end(p, r.e, p.K) - start + 63) >> 6;
         r.row_end = r.row_live = p.M;
     } else {
         tile_coords(t, p, tm, tn);
@@ -761,166 +759,227 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// v[j] += residual[j], 32 values of a row of which `n` are inside the matrix.
-// The row starts on a 16-byte boundary and so does every group of 8; columns
-// past the matrix's edge are not touched, they may lie past the allocation.
-__device__ __forceinline__ void add_residual(float (&v)[32], const __nv_bfloat16* r, int n) {
+// ------------------------------------- epilogue of the modes beyond PLAIN --
+// A lane holds a row; memory wants whole lines.  So a warp's 32 rows x 128 bytes
+// go through 4 KB of shared memory of its own (16-byte unit u of row r at unit
+// u ^ (r & 7): no bank conflicts either way) and leave in ordinary stores, eight
+// lanes to a row's 128-byte line.
+__device__ __forceinline__ uint32_t staged(uint32_t buf, int row, int unit) {
+    return buf + row * 128 + ((unit ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void stage64(uint32_t buf, int lane, int half, const uint32_t* w) {   // this lane's row, 64 bytes
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        if (8 * g + 8 <= n) {
-            const uint4 w = *reinterpret_cast<const uint4*>(r + 8 * g);
-            v[8 * g] += bf16_lo(w.x);
-            v[8 * g + 1] += bf16_hi(w.x);
-            v[8 * g + 2] += bf16_lo(w.y);
-            v[8 * g + 3] += bf16_hi(w.y);
-            v[8 * g + 4] += bf16_lo(w.z);
-            v[8 * g + 5] += bf16_hi(w.z);
-            v[8 * g + 6] += bf16_lo(w.w);
-            v[8 * g + 7] += bf16_hi(w.w);
-        } else {
+    for (int u = 0; u < 4; ++u)
+        sts128(staged(buf, lane, 4 * half + u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+}
+// p: first column of row 0; n: columns, rows: rows that exist.
+template <typename T>
+__device__ __forceinline__ void unstage(T* p, int64_t ld, int n, int rows, uint32_t buf, int lane) {
+    constexpr int kUnit = 16 / sizeof(T);
+    const int unit = lane & 7, c = unit * kUnit;
+    __syncwarp();
+    p += (lane >> 3) * ld + c;
+    if (n >= 8 * kUnit && rows >= 32) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * g + e < n) v[8 * g + e] += __bfloat162float(r[8 * g + e]);
+        for (int k = 0; k < 8; ++k) {
+            *reinterpret_cast<uint4*>(p) = lds128(staged(buf, 4 * k + (lane >> 3), unit));
+            p += 4 * ld;
+        }
+    } else {
+#pragma unroll 1
+        for (int r = lane >> 3; r < rows && r < 32; r += 4) {
+            const uint4 v = lds128(staged(buf, r, unit));
+            if (c + kUnit <= n) {
+                *reinterpret_cast<uint4*>(p) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < kUnit; ++e)
+                    if (c + e < n) {
+                        if constexpr (sizeof(T) == 4) p[e] = __uint_as_float(w[e]);
+                        else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                    }
+            }
+            p += 4 * ld;
+        }
+    }
+    __syncwarp();
+}
+// The residual's 32 values; columns past the matrix's edge are not touched,
+// they may lie past the allocation.
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, uint32_t (&w)[16], int n) {
+    if (n >= 32) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[g];
+            w[4 * g] = v.x;
+            w[4 * g + 1] = v.y;
+            w[4 * g + 2] = v.z;
+            w[4 * g + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * e;
+            w[e] = (2 * e < n ? q[0] : 0u) | (uint32_t)(2 * e + 1 < n ? q[1] : 0u) << 16;
         }
     }
 }
-
-// Store a chunk of which only the first n columns lie inside the matrix.  A
-// bulk tensor store writes whole 16-byte units (the columns past the edge in
-// the last one as zeros), so a chunk that ends inside one goes out with plain
-// stores: what lies behind the matrix's columns stays as it was.
-template <typename T, bool PLANES>
-__device__ __forceinline__ void put_chunk(const CUtensorMap* map, T* base, int64_t ld, uint32_t buf, int lane,
-                                          const uint32_t (&w)[16], int col, int n, int row0, int row_end, int64_t plane_rows,
-                                          int plane, bool& first) {
-    constexpr int kUnit = 16 / sizeof(T);
-    if (n >= 4 * kUnit || n % kUnit == 0) {
-        store_chunk<PLANES>(map, buf, lane, w, col, row0, plane, first);
-        first = false;
-    } else if (row0 + lane < row_end) {
-        T* p = base + (plane * plane_rows + row0 + lane) * ld + col;
-#pragma unroll
-        for (int j = 0; j < 4 * kUnit; ++j)
-            if (j < n) {
-                if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
-                else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-            }
-    }
-}
-
-// Epilogue of the modes beyond PLAIN, one column half of a tile for the
-// calling warp's 32 rows: per 32 columns TMEM -> registers, scales and bias,
-// pre-activation out, activation, residual, out.  The pre-activation is
-// rounded to bf16 where it is stored; the activation takes the binary32 value,
-// so C is rounded once.
-template <int MODE>
+// One column half of a tile for the calling warp's 32 rows: TMEM -> registers,
+// all 128 columns at once, so that the accumulator is free for the next tile's
+// MMAs after one round trip and everything else runs beside them; then per 32
+// columns scale and bias in one fused multiply-add (the bias in shared
+// memory, fetched before the wait), pre-activation out, activation,
+// residual, out.  The pre-activation is rounded to bf16 where it is stored;
+// the activation takes the binary32 value, so C is rounded once.
+// Two of these warps share an issue slot, so what counts is the number of
+// instructions: pairs of columns go through the two-wide multiply and add, and
+// the activation is a template parameter.
+template <int MODE, int ACT>
 __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, int half, int q, int lane, uint32_t rank,
                                              uint32_t tmem, uint32_t bar_tfull, uint32_t bar_tempty,
                                              uint32_t& acc_phase, volatile int* abort_flag, uint32_t& amax_acc,
-                                             const CUtensorMap* map_c, const CUtensorMap* map_pre, uint32_t buf,
-                                             float* s_bias, bool& first) {
-    const int row0 = t.m0 + (int)rank * 128 + q * 32, row = row0 + lane;
+                                             __nv_bfloat16* s_bias, uint32_t buf) {
+    const int row0 = t.m0 + (int)rank * 128 + q * 32;
     const int col0 = t.n0 + half * 128;
-    const int ncols = p.N - col0;
-    const bool store = row0 < t.row_end && ncols > 0;
-    const bool on = row < t.row_live;
-    const int plane = MODE == KSEG ? t.e : 0;
+    const int ncols = p.N - col0, rows = t.row_end - row0;
+    const bool dead = row0 + lane >= t.row_live;    // a row of zeros
+    const bool some_dead = row0 + 32 > t.row_live;  // the same in every lane
+    const int64_t row = (MODE == KSEG ? (int64_t)t.e * p.M : 0) + row0;   // of C
+    uint8_t* c_row = static_cast<uint8_t*>(p.c) + (row * p.ldc + col0) * (p.out_bf16 ? 2 : 4);
+    __nv_bfloat16* pre = p.pre + row * p.ldp + col0;   // not followed where there is none
+    const __nv_bfloat16* residual = p.residual + (row + lane) * p.ldr + col0;
     const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + ACC_COL + half * 128;
-    const float2 alpha = out_scales(p, MODE == ROWS ? min(t.e, p.experts - 1) : 0);
-    if (MODE != KSEG && p.bias) {
-        const __nv_bfloat16* b = p.bias + (int64_t)min(t.e, p.experts - 1) * p.N + col0;
+    const int expert = MODE == ROWS ? min(t.e, p.experts - 1) : 0;
+    float2 alpha = out_scales(p, expert);
+    if (MODE != KSEG) {
+        const __nv_bfloat16* b = p.bias + (int64_t)expert * p.N + col0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s_bias[32 * c + lane] = 32 * c + lane < ncols ? __bfloat162float(b[32 * c + lane]) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            const int c = 32 * i + lane;
+            s_bias[c] = p.bias && c < ncols ? b[c] : __float2bfloat16_rn(0.0f);
+        }
         __syncwarp();
     }
     if (!mbar_wait_cluster(bar_tfull, acc_phase, abort_flag)) return false;
     tc_fence_after();
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        float v[32];
-        if (t.k_steps) {
-            uint32_t u[32];
-            tc_ld_32x32b_x32(taddr + 32 * i, u);
-            tc_wait_ld();
+    float2 u[4][16];
+    if (t.k_steps) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float2 f = scale_out2(u[2 * j], u[2 * j + 1], alpha);
-                v[2 * j] = f.x;
-                v[2 * j + 1] = f.y;
-            }
-        } else {
+        for (int i = 0; i < 4; ++i) tc_ld_32x32b_x32(taddr + 32 * i, reinterpret_cast<uint32_t(&)[32]>(u[i]));
+        tc_wait_ld();
+    } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-        }
-        if (i == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive(bar_tempty);
-                else mbar_arrive_cluster(bar_tempty, 0);
-            }
-            acc_phase ^= 1;
-        }
-        if (!store || 32 * i >= ncols) continue;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[i][j] = make_float2(0.0f, 0.0f);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        if (rank == 0) mbar_arrive(bar_tempty);
+        else mbar_arrive_cluster(bar_tempty, 0);
+    }
+    acc_phase ^= 1;
+    if (rows <= 0) return true;
+    if (alpha.y != 1.0f) {   // the two global scales one after the other, see out_scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[i][j] = __fmul2_rn(u[i][j], make_float2(alpha.x, alpha.x));
+        alpha.x = alpha.y;
+    }
+    const float2 scale = make_float2(alpha.x, alpha.x);
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {   // 64 columns
+        const int n = ncols - 32 * g;  // as many of them inside the matrix
+        if (n <= 0) break;
         uint32_t w[16];
         if constexpr (MODE != KSEG) {
-            if (p.bias) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 b = *reinterpret_cast<const float4*>(s_bias + 32 * i + 4 * j);
-                    v[4 * j] += b.x;
-                    v[4 * j + 1] += b.y;
-                    v[4 * j + 2] += b.z;
-                    v[4 * j + 3] += b.w;
+            for (int i = g; i < g + 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const uint4 b = *reinterpret_cast<const uint4*>(s_bias + 32 * i + 2 * j);
+                    u[i][j] = __ffma2_rn(u[i][j], scale, make_float2(bf16_lo(b.x), bf16_hi(b.x)));
+                    u[i][j + 1] = __ffma2_rn(u[i][j + 1], scale, make_float2(bf16_lo(b.y), bf16_hi(b.y)));
+                    u[i][j + 2] = __ffma2_rn(u[i][j + 2], scale, make_float2(bf16_lo(b.z), bf16_hi(b.z)));
+                    u[i][j + 3] = __ffma2_rn(u[i][j + 3], scale, make_float2(bf16_lo(b.w), bf16_hi(b.w)));
+                }
+                if (p.pre) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = pack_bf16(u[i][j].x, u[i][j].y);
+                    if (some_dead && dead) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = 0u;
+                    }
+                    stage64(buf, lane, i - g, w);
                 }
             }
-            if (p.pre) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = on ? pack_bf16(v[2 * j], v[2 * j + 1]) : 0u;
-                put_chunk<__nv_bfloat16, false>(map_pre, p.pre, p.ldp, buf, lane, w, col0 + 32 * i, ncols - 32 * i, row0,
-                                                t.row_end, 0, 0, first);
-            }
-            apply_act(p.act, v);
-            if (p.residual && on) add_residual(v, p.residual + (int64_t)row * p.ldr + col0 + 32 * i, ncols - 32 * i);
+            if (p.pre) unstage(pre + 32 * g, p.ldp, n, rows, buf, lane);
         }
-        if (p.out_bf16) {
-            uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                w[j] = on ? pack_bf16(v[2 * j], v[2 * j + 1]) : 0u;
-                const int c = 32 * i + 2 * j;
-                m = absmax2(m, c + 1 < ncols ? w[j] : c < ncols ? w[j] & 0xFFFFu : 0u);
-            }
-            amax_acc = max(amax_acc, absmax2_fold(m));
-            put_chunk<__nv_bfloat16, MODE == KSEG>(map_c, reinterpret_cast<__nv_bfloat16*>(p.c), p.ldc, buf, lane, w,
-                                                   col0 + 32 * i, ncols - 32 * i, row0, t.row_end, p.M, plane, first);
-        } else {
-            float fmax = 0.0f;
+        for (int i = g; i < g + 2; ++i) {
+            const int ni = n - 32 * (i - g);
+            float2* v = u[i];
+            if constexpr (MODE != KSEG) {
+                uint32_t res[16];
+                if (p.residual && !dead) load_row(residual + 32 * i, res, ni);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int j = 0; j < 16; ++j) v[j] = act_value2<ACT>(v[j]);
+                if (p.residual && !dead) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float f = on ? v[16 * h + j] : 0.0f;
-                    w[j] = __float_as_uint(f);
-                    if (32 * i + 16 * h + j < ncols) fmax = fmaxf(fmax, fabsf(f));
+                    for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], make_float2(bf16_lo(res[j]), bf16_hi(res[j])));
                 }
-                if (32 * i + 16 * h < ncols)
-                    put_chunk<float, MODE == KSEG>(map_c, reinterpret_cast<float*>(p.c), p.ldc, buf, lane, w,
-                                                   col0 + 32 * i + 16 * h, ncols - 32 * i - 16 * h, row0, t.row_end, p.M,
-                                                   plane, first);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __fmul2_rn(v[j], scale);
             }
-            amax_acc = max(amax_acc, __float_as_uint(fmax));
+            if (some_dead && dead) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = make_float2(0.0f, 0.0f);
+            }
+            if (p.out_bf16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[j].x, v[j].y);
+                if (p.c_amax) {
+                    uint32_t m = 0;
+                    if (ni >= 32) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) m = absmax2(m, w[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            m = absmax2(m, 2 * j + 1 < ni ? w[j] : 2 * j < ni ? w[j] & 0xFFFFu : 0u);
+                    }
+                    amax_acc = max(amax_acc, absmax2_fold(m));
+                }
+                stage64(buf, lane, i - g, w);
+            } else {
+                if (p.c_amax) {
+                    float peak = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (2 * j < ni) peak = fmaxf(peak, fabsf(v[j].x));
+                        if (2 * j + 1 < ni) peak = fmaxf(peak, fabsf(v[j].y));
+                    }
+                    amax_acc = max(amax_acc, __float_as_uint(peak));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) stage64(buf, lane, h, reinterpret_cast<const uint32_t*>(v) + 16 * h);
+                unstage(reinterpret_cast<float*>(c_row) + 32 * i, p.ldc, ni, rows, buf, lane);
+            }
         }
+        if (p.out_bf16) unstage(reinterpret_cast<__nv_bfloat16*>(c_row) + 32 * g, p.ldc, n, rows, buf, lane);
     }
     __syncwarp();   // s_bias has been read
     return true;
 }
 
-template <bool MX, int MODE>
-__global__ void __launch_bounds__(P_NUM_THREADS, 1)
+template <bool MX, int MODE, int ACT = ACT_NONE>
+__global__ void __launch_bounds__(MODE == PLAIN ? P_NUM_THREADS : X_NUM_THREADS, 1)
 gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pre,
-                      KParams p) {
+                      const __grid_constant__ CUtensorMap map_c, KParams p) {   // map_c: MODE PLAIN only
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -934,9 +993,10 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P_OFF_MISC + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kScaleWarp = MODE == PLAIN ? 2 : 4, kEpilogueWarp = MODE == PLAIN ? 6 : 8;   // the first of each
     const uint32_t rank = cluster_rank();
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
-    const Groups groups = groups_at(smem);   // MODE ROWS and KSEG only
+    const Groups groups = groups_at(smem);   // MODE ROWS only
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P_STAGES; ++s) {
@@ -951,7 +1011,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if ((MODE == ROWS || MODE == KSEG) && warp == 2) fill_groups(groups, p, MODE == ROWS ? p.M : p.K, lane);
+    if (MODE == ROWS && warp == kScaleWarp) fill_groups(groups, p, lane);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS));
@@ -964,6 +1024,8 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     const uint32_t tmem = *tmem_slot;
     const int num_tiles = tile_count<MODE>(p, groups);
 
+    if (warp < kEpilogueWarp) {
+    if constexpr (MODE != PLAIN) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X_REGS_OTHERS));
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
         if (lane == 0) {
@@ -1046,7 +1108,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
             const unsigned long long t0 = globaltimer();
             while (!mbar_try_cluster(bar_drain, 0) && globaltimer() - t0 < kWaitLimitNs) {}
         }
-    } else if (warp < 6) {
+    } else if (warp >= kScaleWarp) {
         // -------------------------------------------------- scales -> TMEM ----
         // Warp q of this group owns TMEM lanes 32q..32q+31 (q = warp % 4) and
         // does nothing else, so the block scales of the next stages are in
@@ -1092,13 +1154,16 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
                 if (++s == P_STAGES) { s = 0; phase ^= 1; }
             }
         }
+    }
     } else {
+        if constexpr (MODE != PLAIN) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X_REGS_EPILOGUE));
         // ----------------------------------------------------------- epilogue ----
-        // warps 6..9: columns 0..127, warps 10..13: columns 128..255, of the
+        // the first four: columns 0..127, the others: columns 128..255, of the
         // TMEM lane quarter warp % 4
-        const int q = warp & 3, half = (warp - 6) >> 2;
+        const int q = warp & 3, half = (warp - kEpilogueWarp) >> 2;
         const float2 alpha = MODE == PLAIN ? out_scales(p, 0) : make_float2(0.0f, 0.0f);
-        const uint32_t buf = sbase + P_OFF_EPI + (warp - 6) * EPI_BUF;
+        const uint32_t buf = sbase + (MODE == PLAIN ? P_OFF_EPI : X_OFF_EPI) +
+                             (warp - kEpilogueWarp) * (MODE == PLAIN ? EPI_BUF : X_EPI_BUF);
         uint32_t acc_phase = 0;
         uint32_t amax_acc = 0;
         bool first = true;
@@ -1107,13 +1172,12 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
                 if (!epilogue_half_pair(p, tile, half, q, lane, rank, tmem, alpha, bar_tfull, bar_tempty, acc_phase,
                                         abort_flag, amax_acc, &map_c, buf, first)) break;
             } else {
-                float* s_bias = reinterpret_cast<float*>(smem + X_OFF_BIAS) + (warp - 6) * 128;
-                if (!epilogue_ext<MODE>(p, tile_at<MODE>(tile, p, groups), half, q, lane, rank, tmem, bar_tfull,
-                                        bar_tempty, acc_phase, abort_flag, amax_acc, &map_c, &map_pre, buf, s_bias,
-                                        first)) break;
+                __nv_bfloat16* s_bias = reinterpret_cast<__nv_bfloat16*>(smem + X_OFF_BIAS) + (warp - kEpilogueWarp) * 128;
+                if (!epilogue_ext<MODE, ACT>(p, tile_at<MODE>(tile, p, groups), half, q, lane, rank, tmem, bar_tfull,
+                                             bar_tempty, acc_phase, abort_flag, amax_acc, s_bias, buf)) break;
             }
         }
-        if (lane == 0) bulk_wait0();    // every store of this warp has completed
+        if (MODE == PLAIN && lane == 0) bulk_wait0();    // every store of this warp has completed
         __syncwarp();
         if (p.c_amax) amax_publish(p.c_amax, amax_acc);
     }
@@ -1173,18 +1237,34 @@ bool make_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t k,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// planes > 0: a stack of `planes` such matrices.
-bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ldc, bool bf16, int64_t planes = 0) {
+bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ldc, bool bf16) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int esz = bf16 ? 2 : 4;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    cuuint64_t strides[2] = {(cuuint64_t)(ldc * esz), (cuuint64_t)(rows * ldc * esz)};
-    cuuint32_t box[3] = {(cuuint32_t)(64 / esz), 32, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes ? 3 : 2, base, dims, strides, box, estr,
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(ldc * esz)};
+    cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef void (*PairKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, KParams);
+
+template <int MODE>
+PairKernel act_kernel(int act) {
+    switch (act) {
+        case ACT_RELU: return gemm_nvf4_pair_kernel<false, MODE, ACT_RELU>;
+        case ACT_RELU2: return gemm_nvf4_pair_kernel<false, MODE, ACT_RELU2>;
+        case ACT_GELU: return gemm_nvf4_pair_kernel<false, MODE, ACT_GELU>;
+        case ACT_GELU_TANH: return gemm_nvf4_pair_kernel<false, MODE, ACT_GELU_TANH>;
+        case ACT_SILU: return gemm_nvf4_pair_kernel<false, MODE, ACT_SILU>;
+        default: return gemm_nvf4_pair_kernel<false, MODE, ACT_NONE>;
+    }
+}
+PairKernel ext_kernel(int mode, int act) {
+    return mode == KSEG ? gemm_nvf4_pair_kernel<false, KSEG> : mode == ROWS ? act_kernel<ROWS>(act) : act_kernel<EPILOGUE>(act);
 }
 
 struct DeviceInfo {
@@ -1209,11 +1289,12 @@ DeviceInfo device_info() {
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_BYTES);
             cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
         }
-        for (auto k : {gemm_nvf4_pair_kernel<false, EPILOGUE>, gemm_nvf4_pair_kernel<false, ROWS>,
-                       gemm_nvf4_pair_kernel<false, KSEG>}) {
-            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, X_SMEM_BYTES);
-            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
-        }
+        for (int mode : {EPILOGUE, ROWS, KSEG})
+            for (int act = 0; act < (mode == KSEG ? 1 : kNumActivations); ++act) {
+                PairKernel k = ext_kernel(mode, act);
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, X_SMEM_BYTES);
+                cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
+            }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (n / 2));
         cfg.blockDim = dim3(P_NUM_THREADS);
@@ -1246,13 +1327,11 @@ int group_for(int64_t rows_per_tile, int64_t K, int tiles_m) {
     return (int)gm;
 }
 
-typedef void (*PairKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, KParams);
-
-cudaError_t launch_pairs(PairKernel kernel, int clusters, int smem, cudaStream_t s, const CUtensorMap& ma,
-                         const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mp, const KParams& p) {
+cudaError_t launch_pairs(PairKernel kernel, int clusters, int threads, int smem, cudaStream_t s, const CUtensorMap& ma,
+                         const CUtensorMap& mb, const CUtensorMap& mc, const KParams& p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(P_NUM_THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1262,7 +1341,7 @@ cudaError_t launch_pairs(PairKernel kernel, int clusters, int smem, cudaStream_t
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, mp, p);
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, p);
 }
 
 }  // namespace
@@ -1309,8 +1388,8 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
     p.group_m = group_for(256, g.K, p.tiles_m);
     const int tiles = p.tiles_m * p.tiles_n;
     const int clusters = tiles < dev.pair_clusters ? tiles : dev.pair_clusters;
-    return p.mx ? launch_pairs(gemm_nvf4_pair_kernel<true, PLAIN>, clusters, P_SMEM_BYTES, s, ma, mb, mc, mc, p)
-                : launch_pairs(gemm_nvf4_pair_kernel<false, PLAIN>, clusters, P_SMEM_BYTES, s, ma, mb, mc, mc, p);
+    return p.mx ? launch_pairs(gemm_nvf4_pair_kernel<true, PLAIN>, clusters, P_NUM_THREADS, P_SMEM_BYTES, s, ma, mb, mc, p)
+                : launch_pairs(gemm_nvf4_pair_kernel<false, PLAIN>, clusters, P_NUM_THREADS, P_SMEM_BYTES, s, ma, mb, mc, p);
 }
 
 cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
@@ -1329,7 +1408,6 @@ cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
     p.bias = static_cast<const __nv_bfloat16*>(g.bias);
     p.residual = static_cast<const __nv_bfloat16*>(g.residual);
     p.ldr = g.ldr;
-    p.act = g.act;
     p.pre = static_cast<__nv_bfloat16*>(g.pre);
     p.ldp = g.ldp;
     p.c = g.c;
@@ -1340,21 +1418,17 @@ cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
     p.sfb_stride = (int64_t)mma_scale_bytes(g.N, g.K);
     p.tiles_n = (int)ceil_div(g.N, BN);
     const bool rows = g.offsets && !g.wgrad;
-    CUtensorMap ma, mb, mc, mp;
-    if (!make_code_map(&ma, g.a, g.M, g.K, 128) || !make_code_map(&mb, g.b, rows ? g.experts * g.N : g.N, g.K, 128) ||
-        !make_out_map(&mc, g.c, g.M, g.N, g.ldc, g.out_bf16 != 0, g.wgrad ? g.experts : 0) ||
-        (g.pre && !make_out_map(&mp, g.pre, g.M, g.N, g.ldp, true)))
+    CUtensorMap ma, mb;
+    if (!make_code_map(&ma, g.a, g.M, g.K, 128) || !make_code_map(&mb, g.b, rows ? g.experts * g.N : g.N, g.K, 128))
         return cudaErrorInvalidValue;
-    if (!g.pre) mp = mc;
     p.tiles_m = (int)ceil_div(g.M, 256);
     p.group_m = group_for(256, g.wgrad ? ceil_div(g.K, g.experts) : g.K, p.tiles_m);   // an average segment
     // ROWS: how the rows fall into segments is known on the device only; at
     // most, every 128 rows are a tile of their own.
     const int64_t tiles = (rows ? ceil_div(g.M, 128) : p.tiles_m) * p.tiles_n * (g.wgrad ? g.experts : 1);
     const int clusters = (int)(tiles < dev.pair_clusters ? tiles : dev.pair_clusters);
-    auto kernel = g.wgrad ? gemm_nvf4_pair_kernel<false, KSEG>
-                          : rows ? gemm_nvf4_pair_kernel<false, ROWS> : gemm_nvf4_pair_kernel<false, EPILOGUE>;
-    return launch_pairs(kernel, clusters, X_SMEM_BYTES, s, ma, mb, mc, mp, p);
+    PairKernel kernel = ext_kernel(g.wgrad ? KSEG : rows ? ROWS : EPILOGUE, g.act);
+    return launch_pairs(kernel, clusters, X_NUM_THREADS, X_SMEM_BYTES, s, ma, mb, ma, p);
 }
 
 unsigned int read_and_clear_error_word(cudaStream_t s, cudaError_t* err) {

@@ -92,7 +92,8 @@ struct GemmExtArgs {
     int wgrad;
 };
 cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s);
-constexpr int64_t kMaxExpertsArg = 1024;
+constexpr int64_t kMaxExpertsArg = 512;
+constexpr int64_t kMaxSortedRows = 1 << 23;   // rows of a product over sorted rows: its tiles are counted in 16 bits
 
 struct ActGradArgs {
     const void* dy;

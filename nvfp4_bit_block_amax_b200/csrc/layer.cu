@@ -448,73 +448,84 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
     }
 }
 
-// The gradient of combine.  A CTA takes one token: its row of dout is read
-// once, each copy's row of dy is written, each copy's row of y is read for
-// dweights = <dout, y> (8 copies at a time; a thread's binary32 partial sums
-// are added over lanes, then over warps in order).  Further units zero the
-// rows that hold no copy.
-constexpr int kDots = 8;
+// The gradient of combine.  WARPS warps (1, or the CTA's 8) take up to 4 copies
+// of one token: its row of dout is read (by a second group of 4 from L2), each
+// copy's row of dy is written, each copy's row of y is read for dweights =
+// <dout, y>.  A lane's binary32 partial sums are added over lanes, then over
+// warps in order.  Further units zero the rows that hold no copy.  One warp per
+// unit needs no block-wide step and serves many tokens; with few, 8 warps share
+// a row, so that its loads are all in flight at once.
+constexpr int kDots = 4;
 
+template <int WARPS>
 __global__ void __launch_bounds__(kThreads) combine_grad_kernel(MoveParams p) {
     __shared__ float s_dot[kWarps][kDots];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t zeros = (zero_units(p) + kWarps - 1) / kWarps;
+    const int sub = WARPS == 1 ? 0 : warp;
+    const int groups = (p.topk + kDots - 1) / kDots;
+    const int64_t units = p.tokens * groups, all = units + (zero_units(p) + WARPS - 1) / WARPS;
     const bool dots = p.dweights != nullptr;
     uint32_t peak = 0;
-    for (int64_t u = blockIdx.x; u < p.tokens + zeros; u += gridDim.x) {
-        if (u >= p.tokens) {
-            const int64_t z = (u - p.tokens) * kWarps + warp;
+    const int64_t first = WARPS == 1 ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x;
+    for (int64_t u = first; u < all; u += (int64_t)gridDim.x * (kWarps / WARPS)) {
+        if (u >= units) {
+            const int64_t z = (u - units) * WARPS + sub;
             if (z < zero_units(p)) zero_unit(p, z, lane);
             continue;
         }
-        for (int j0 = 0; j0 < p.topk; j0 += kDots) {
-            const int64_t copy0 = u * p.topk + j0;
-            const int m = min(kDots, p.topk - j0);
-            int row[kDots];
-            float w[kDots], dot[kDots];
+        const int64_t t = u / groups;
+        const int j0 = (int)(u - t * groups) * kDots, m = min(kDots, p.topk - j0);
+        const int64_t copy0 = t * p.topk + j0;
+        int row[kDots];
+        float w[kDots], dot[kDots];
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) {
+            row[j] = j < m ? row_of(p, copy0 + j) : -1;
+            w[j] = j < m && p.weights ? __ldg(p.weights + copy0 + j) : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t c = 8 * (sub * 32 + lane); c < p.cols; c += 8 * 32 * WARPS) {
+            const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.src + t * p.lds + c));
+            uint4 y[kDots];
+#pragma unroll
+            for (int j = 0; j < kDots; ++j)
+                if (dots && row[j] >= 0) y[j] = ldg_stream(p.other + row[j] * p.ldo + c);
+            float f[8];
+            unpack8(g, f);
 #pragma unroll
             for (int j = 0; j < kDots; ++j) {
-                row[j] = j < m ? row_of(p, copy0 + j) : -1;
-                w[j] = j < m && p.weights ? __ldg(p.weights + copy0 + j) : 1.0f;
-                dot[j] = 0.0f;
+                if (row[j] < 0) continue;
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = w[j] * f[e];
+                const uint4 d = pack8(o);
+                peak = absmax8(peak, d);
+                *reinterpret_cast<uint4*>(p.dst + row[j] * p.ldd + c) = d;
+                if (dots) {
+                    unpack8(y[j], o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[j] = fmaf(o[e], f[e], dot[j]);
+                }
             }
-            for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
-                const uint4 g = ldg_stream(p.src + u * p.lds + c);
-                uint4 y[kDots];
+        }
+        if (dots) {
+#pragma unroll
+            for (int j = 0; j < kDots; ++j)
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+            if constexpr (WARPS == 1) {
 #pragma unroll
                 for (int j = 0; j < kDots; ++j)
-                    if (dots && row[j] >= 0) y[j] = ldg_stream(p.other + row[j] * p.ldo + c);
-                float f[8];
-                unpack8(g, f);
+                    if (lane == j && j < m) p.dweights[copy0 + j] = dot[j];
+            } else {
 #pragma unroll
-                for (int j = 0; j < kDots; ++j) {
-                    if (row[j] < 0) continue;
-                    float o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = w[j] * f[e];
-                    const uint4 d = pack8(o);
-                    peak = absmax8(peak, d);
-                    *reinterpret_cast<uint4*>(p.dst + row[j] * p.ldd + c) = d;
-                    if (dots) {
-                        unpack8(y[j], o);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(o[e], f[e], dot[j]);
-                    }
-                }
-            }
-            if (dots) {
-#pragma unroll
-                for (int j = 0; j < kDots; ++j) {
-                    if (j >= m) break;
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+                for (int j = 0; j < kDots; ++j)
                     if (lane == 0) s_dot[warp][j] = dot[j];
-                }
                 __syncthreads();
                 if (threadIdx.x < m) {
-                    float t = 0.0f;
-                    for (int v = 0; v < kWarps; ++v) t += s_dot[v][threadIdx.x];
-                    p.dweights[copy0 + threadIdx.x] = t;
+                    float s = 0.0f;
+                    for (int v = 0; v < kWarps; ++v) s += s_dot[v][threadIdx.x];
+                    p.dweights[copy0 + threadIdx.x] = s;
                 }
                 __syncthreads();
             }
@@ -656,8 +667,11 @@ cudaError_t launch_moe_combine(const MoveArgs& a, cudaStream_t s, int* launches)
 cudaError_t launch_moe_combine_grad(const MoveArgs& a, cudaStream_t s, int* launches) {
     cudaError_t e = zero_word(a.amax, s);
     if (e != cudaSuccess) return e;
-    const int64_t units = a.tokens + ceil_div(zero_units_host(a), kWarps);
-    combine_grad_kernel<<<grid_for_units(units), kThreads, 0, s>>>(move_params(a));
+    const int64_t units = a.tokens * ceil_div(a.topk, kDots), zeros = zero_units_host(a);
+    if (units >= 16 * (int64_t)sm_count())
+        combine_grad_kernel<1><<<grid_for_units(ceil_div(units + zeros, kWarps)), kThreads, 0, s>>>(move_params(a));
+    else
+        combine_grad_kernel<kWarps><<<grid_for_units(units + ceil_div(zeros, kWarps)), kThreads, 0, s>>>(move_params(a));
     *launches += 1;
     return cudaGetLastError();
 }

@@ -307,8 +307,8 @@ def routing(tokens, topk, experts, seed, skew=2.0, bad=0.0):
     return torch.from_numpy(ids).cuda()
 
 
-SORTS = [(1, 1, 1, 0.0), (1, 1, 1024, 0.0), (3, 2, 2, 0.0), (37, 2, 8, 0.0), (300, 8, 64, 0.05), (1000, 1, 7, 0.3),
-         (1025, 1, 3, 0.0), (5000, 8, 128, 0.01), (20000, 2, 1000, 0.0), (64, 4, 1024, 0.0), (50, 3, 5, 1.0)]
+SORTS = [(1, 1, 1, 0.0), (1, 1, 512, 0.0), (3, 2, 2, 0.0), (37, 2, 8, 0.0), (300, 8, 64, 0.05), (1000, 1, 7, 0.3),
+         (1025, 1, 3, 0.0), (5000, 8, 128, 0.01), (20000, 2, 500, 0.0), (64, 4, 512, 0.0), (50, 3, 5, 1.0)]
 
 
 @pytest.mark.parametrize("tokens,topk,experts,bad", SORTS)

@@ -62,10 +62,10 @@ def test_gemm_grouped(L):
     refused = lambda **kw: call(L.nvfp4_gemm_grouped, d, **kw)
     assert refused(off=None) == ARG and refused(cnt=None) == ARG
     assert refused(off=FAKE + 2) == ALIGN and refused(cnt=FAKE + 1) == ALIGN
-    for e in (0, -1, 1025):
+    for e in (0, -1, 513):
         assert refused(E=e) == ARG
-    assert refused(E=1024, N=1 << 22, ldc=1 << 22, ldr=1 << 22, ldp=1 << 22) == ARG      # E N past 31 bits
-    assert refused(M=192) == SHAPE and refused(M=0) == ARG
+    assert refused(E=512, N=1 << 22, ldc=1 << 22, ldr=1 << 22, ldp=1 << 22) == ARG      # E N past 31 bits
+    assert refused(M=192) == SHAPE and refused(M=0) == ARG and refused(M=(1 << 23) + 128) == SHAPE
 
 
 def test_gemm_grouped_wgrad(L):
@@ -74,7 +74,7 @@ def test_gemm_grouped_wgrad(L):
     for name in OPERANDS:
         assert refused(**{name: None}) == ARG and refused(**{name: FAKE + 2}) == ALIGN
     assert refused(K=192) == SHAPE and refused(K=100) == SHAPE           # segments start at multiples of 128
-    assert refused(E=0) == ARG and refused(E=1025) == ARG and refused(off=None) == ARG and refused(cnt=None) == ARG
+    assert refused(E=0) == ARG and refused(E=513) == ARG and refused(off=None) == ARG and refused(cnt=None) == ARG
     assert refused(ldc=120) == ARG and refused(ldc=132) == ALIGN and refused(c=FAKE + 4) == ALIGN
     assert refused(dt=5) == ARG and refused(M=0) == ARG and refused(N=0) == ARG
 
@@ -89,16 +89,16 @@ def test_act_grad(L):
         assert refused(**{m: None}) == ARG and refused(**{m: FAKE + 8}) == ALIGN
         assert refused(**{ld: 120}) == ARG and refused(**{ld: 132}) == ALIGN
     assert refused(M=0) == ARG and refused(N=0) == ARG and refused(M=1 << 31) == ARG and refused(act=6) == ARG
-    assert refused(E=-1) == ARG and refused(E=2) == ARG and refused(E=1025, off=FAKE, cnt=FAKE) == ARG
+    assert refused(E=-1) == ARG and refused(E=2) == ARG and refused(E=513, off=FAKE, cnt=FAKE) == ARG
     assert refused(E=2, off=FAKE, cnt=FAKE) == SHAPE                     # 300 rows
     assert refused(db=FAKE + 2) == ALIGN and refused(amax=FAKE + 2) == ALIGN
     assert refused(ws=None) == WORK and refused(wsb=need - 1) == WORK and refused(ws=FAKE + 4) == WORK
 
 
 def test_moe_sort(L):
-    assert N.nvfp4_moe_rows(1, 1) == 128 and N.nvfp4_moe_rows(1, 1000) == 128
+    assert N.nvfp4_moe_rows(1, 1) == 128 and N.nvfp4_moe_rows(1, 500) == 128
     assert N.nvfp4_moe_rows(128, 1) == 256               # 128 copies of one expert fit in 128, but 128 + 127 bounds
-    assert N.nvfp4_moe_rows(74, 8) == 1152 and N.nvfp4_moe_rows(0, 4) == 0 and N.nvfp4_moe_rows(4, 1025) == 0
+    assert N.nvfp4_moe_rows(74, 8) == 1152 and N.nvfp4_moe_rows(0, 4) == 0 and N.nvfp4_moe_rows(4, 513) == 0
     need = N.nvfp4_moe_workspace_size(5000, 64)
     assert need >= 64 * 4 and N.nvfp4_moe_workspace_size(0, 1) == 0
     d = dict(ids=FAKE, n=5000, E=64, rows=N.nvfp4_moe_rows(5000, 64), off=FAKE, cnt=FAKE, rc=FAKE, cr=FAKE, ws=FAKE,
@@ -108,7 +108,7 @@ def test_moe_sort(L):
         assert refused(**{name: None}) == ARG and refused(**{name: FAKE + 2}) == ALIGN
     for n in (0, -1, 1 << 31, (1 << 31) - 1):            # the last one's rows pass 31 bits
         assert refused(n=n) == ARG
-    assert refused(E=0) == ARG and refused(E=1025) == ARG and refused(rows=0) == ARG and refused(rows=200) == SHAPE
+    assert refused(E=0) == ARG and refused(E=513) == ARG and refused(rows=0) == ARG and refused(rows=200) == SHAPE
     assert refused(ws=None) == WORK and refused(wsb=need - 4) == WORK and refused(ws=FAKE + 4) == WORK
 
 
