@@ -25,11 +25,12 @@ COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
 UNITS = {
     "quant.cu": ["--fmad=false"],
     "gemm.cu": [],
+    "few.cu": [],
     "mxfp4.cu": [],
     "layer.cu": [],
     "api.cu": [],
 }
-HEADERS = ["activation.cuh", "common.cuh", "internal.h", "tc.cuh"]
+HEADERS = ["activation.cuh", "common.cuh", "internal.h", "segments.cuh", "tc.cuh"]
 
 
 def _nvcc() -> str:

@@ -391,7 +391,8 @@ static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
     if (g.c_amax &&
         cudaMemsetAsync(g.c_amax, 0, sizeof(float), static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    cudaError_t e = launch_gemm_ext(g, static_cast<cudaStream_t>(stream));
+    const bool few = !g.wgrad && (g.experts ? g.M <= 128 * (g.experts + 1) : g.M <= 128);
+    cudaError_t e = (few ? launch_gemm_few : launch_gemm_ext)(g, static_cast<cudaStream_t>(stream));
     g_launches += 1;
     return from_cuda(e);
 }

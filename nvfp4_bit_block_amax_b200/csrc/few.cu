@@ -1,0 +1,413 @@
+// few.cu -- the linear layer's product for few rows (tokens): one to 128, and
+// experts that have about as many rows each.
+//
+// C[t][n] = act(alpha sum_k x_tk w_nk + bias_n) + residual_tn.  With few rows
+// the weight is read once and hardly used: 0.5625 bytes per element against
+// 2 t flops, far on the memory side up to some hundred rows.  So the weight takes
+// the place of the matrix product's wide operand and the tokens that of the
+// narrow one: tcgen05.mma M = 128 features x N = 16 .. 128 tokens, K = 64.
+//   - A CTA takes 128 features and a part of K; the CTAs of a cluster (1 to 8)
+//     share K, so that a small weight still fills the GPU.  Their accumulators
+//     meet in distributed shared memory, tokens dealt to the CTAs, and are
+//     added in the order of the CTAs: no workspace, no atomics, the same
+//     result every time.
+//   - Two CTAs to an SM, each with 72 KB (64 tokens and more: 54 KB) of weight
+//     in flight, several times what hides the latency of HBM.
+//   - Warp 0: TMA producer.  Warp 1: block scales to tensor memory (tcgen05.cp,
+//     which costs the tensor pipe little here) and the MMAs.  Warps 2 .. 5: the
+//     epilogue, a feature to a lane, a token to a column.
+// Every wait is bounded, as in the large product.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "activation.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "segments.cuh"
+#include "tc.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int F_ROWS = 128;                     // features of a CTA
+constexpr int F_BKB = 128;                      // bytes of codes per row and stage: K = 256
+constexpr int F_W_STAGE = F_ROWS * F_BKB;       // 16 KB
+constexpr int F_SF_STAGE = 4 * 512;             // 4 K steps of 128 rows x 4 scales
+constexpr int F_THREADS = 192;
+constexpr uint32_t F_TMEM = 256;
+
+// TOK: most tokens of one pass.
+template <int TOK>
+struct Layout {
+    static constexpr int kStages = TOK == 32 ? 4 : 3;
+    static constexpr int kX = TOK * F_BKB;
+    static constexpr int kStage = F_W_STAGE + kX + 2 * F_SF_STAGE;
+    static constexpr int kOffX = F_W_STAGE, kOffSfw = kOffX + kX, kOffSfx = kOffSfw + F_SF_STAGE;
+    static constexpr int kOffBar = kStages * kStage;   // full, empty per stage; accumulator
+    static constexpr int kOffMisc = kOffBar + (2 * kStages + 2) * 8;
+    static constexpr int kBytes = kOffMisc + 16 + 1008;
+    static constexpr uint32_t kSf = TOK;               // first tensor-memory column of the scales, 32 per stage
+    static_assert(kStage % 1024 == 0 && kSf + kStages * 32 <= F_TMEM, "layout");
+    static_assert((TOK + 8) * F_ROWS * 4 <= kOffBar, "partial sums of a cluster fit in the stages");
+};
+
+struct FewParams {
+    const uint8_t* sfx;
+    const uint8_t* sfw;
+    const float* x_gs;
+    const float* w_gs;
+    int M, N, K;
+    int chunks_k;
+    int tiles;                      // ceil(N / 128)
+    int64_t sfw_stride;             // bytes of one expert's weight scales
+    const int* offsets;             // nullable: rows in expert segments
+    const int* counts;
+    int experts;
+    const __nv_bfloat16* bias;
+    const __nv_bfloat16* residual;
+    int64_t ldr;
+    int out_bf16;
+    void* c;
+    int64_t ldc;
+    __nv_bfloat16* pre;
+    int64_t ldp;
+    unsigned int* c_amax;
+    int act;
+};
+
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t smem) {
+    // 32 rows x 16 bytes, contiguous, no swizzle (8-row groups 128 bytes apart), copied to all four lane quarters
+    const uint64_t desc = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1u << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, float v) {
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+        "st.shared::cluster.f32 [ra], %2;\n\t}"
+        ::"r"(addr), "r"(rank), "f"(v)
+        : "memory");
+}
+
+// One element of C from its sum over K.
+struct Finish {
+    float2 alpha;
+    float bias;
+    int64_t n;      // feature
+    bool on;        // a feature that exists
+};
+template <int ACT>
+__device__ __forceinline__ void finish(const FewParams& p, const Finish& f, int64_t row, float sum, uint32_t& amax) {
+    if (!f.on) return;
+    const float z = fmaf(sum * f.alpha.x, f.alpha.y, f.bias);
+    if (p.pre) p.pre[row * p.ldp + f.n] = __float2bfloat16_rn(z);
+    float v = act_value<ACT>(z);
+    if (p.residual) v += __bfloat162float(p.residual[row * p.ldr + f.n]);
+    if (p.out_bf16) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        static_cast<__nv_bfloat16*>(p.c)[row * p.ldc + f.n] = h;
+        v = __bfloat162float(h);
+    } else {
+        static_cast<float*>(p.c)[row * p.ldc + f.n] = v;
+    }
+    amax = max(amax, __float_as_uint(fabsf(v)));
+}
+
+template <int TOK, int ACT>
+__global__ void __launch_bounds__(F_THREADS, 2)
+gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, FewParams p) {
+    using L = Layout<TOK>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + L::kOffBar, bar_empty = bar_full + 8 * L::kStages;
+    const uint32_t bar_acc = bar_empty + 8 * L::kStages, bar_drain = bar_acc + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank(), splits = (int)cluster_size();
+    const int unit = blockIdx.x / splits;
+    const int e = unit / p.tiles, tile = unit - e * p.tiles;
+    const int start = p.offsets ? segment_start(p.offsets, e, p.M) : 0;
+    const int stop = p.offsets ? segment_end(p.offsets, p.counts, e, p.M) : p.M;
+    const int n0 = tile * F_ROWS;
+    const int steps = p.K / 64, blocks = (steps + 3) / 4;
+    const int kb0 = (int)((int64_t)blocks * rank / splits), kb1 = (int)((int64_t)blocks * (rank + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        mbar_init(bar_acc, 1);
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(F_TMEM));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    Finish f{};
+    if (warp >= 2) {
+        f.n = n0 + (warp & 3) * 32 + lane;
+        f.on = f.n < p.N;
+        const float sx = __ldg(p.x_gs), sw = __ldg(p.w_gs + e), a = __fmul_rn(sx, sw);
+        // as the large product: one factor, or two where it leaves the normal range
+        f.alpha = a >= 0x1p-126f && a <= 0x1.fffffep127f ? make_float2(a, 1.0f) : make_float2(sx, sw);
+        f.bias = p.bias && f.on ? __bfloat162float(p.bias[(int64_t)e * p.N + f.n]) : 0.0f;
+    }
+    uint32_t amax = 0;
+    int s = 0;                      // stage and its phase, of the producer and of the MMA role
+    uint32_t phase = 0, acc_phase = 0;
+    uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
+    bool ok = true;
+    for (int t0 = start; t0 < stop; t0 += TOK) {      // a pass over the weight for up to TOK tokens
+        const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
+        if (warp == 0) {
+            if (lane == 0) {
+                const uint8_t* sfw = p.sfw + e * p.sfw_stride + (int64_t)tile * p.chunks_k * 512;
+                const uint8_t* sfx = p.sfx + (int64_t)(t0 >> 7) * p.chunks_k * 512;
+                for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                    if (!mbar_wait(bar_empty + 8 * s, phase ^ 1, abort_flag)) { ok = false; break; }
+                    const int nk = min(4, steps - kb * 4);
+                    const uint32_t full = bar_full + 8 * s, at = sbase + s * L::kStage;
+                    mbar_expect_tx(full, (uint32_t)(F_W_STAGE + boxes * 16 * F_BKB + 2 * nk * 512));
+                    tma_load_2d(at, &map_w, full, kb * F_BKB, e * p.N + n0);
+                    bulk_load(at + L::kOffSfw, sfw + (int64_t)kb * 2048, nk * 512, full);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(at + L::kOffX + b * 16 * F_BKB, &map_x, full, kb * F_BKB, t0 + 16 * b);
+                    bulk_load(at + L::kOffSfx, sfx + (int64_t)kb * 2048, nk * 512, full);
+                    issued_any |= 1u << s;
+                    issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
+                    if (++s == L::kStages) { s = 0; phase ^= 1; }
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                const uint32_t idesc =
+                    (1u << 7) | (1u << 10) | ((uint32_t)(16 * boxes >> 3) << 17) | ((uint32_t)(F_ROWS >> 4) << 24);
+                for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                    if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const int nk = min(4, steps - kb * 4);
+                    const uint32_t at = sbase + s * L::kStage, sf = tmem + L::kSf + s * 32;
+                    for (int j = 0; j < nk; ++j) {
+                        cp_scales(sf + 4 * j, at + L::kOffSfw + 512 * j);
+                        cp_scales(sf + 16 + 4 * j, at + L::kOffSfx + 512 * j);
+                    }
+                    for (int j = 0; j < nk; ++j)
+                        tc_mma_nvf4(tmem, desc_sw128(at + j * 32), desc_sw128(at + L::kOffX + j * 32), idesc, sf + 4 * j,
+                                    sf + 16 + 4 * j, kb > kb0 || j > 0, false);
+                    tc_commit(bar_empty + 8 * s);
+                    if (++s == L::kStages) { s = 0; phase ^= 1; }
+                }
+                tc_commit(bar_acc);
+            }
+        } else {
+            ok = mbar_wait(bar_acc, acc_phase, abort_flag) && ok;
+            tc_fence_after();
+        }
+        acc_phase ^= 1;
+        __syncwarp();
+        const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        if (splits == 1) {
+            if (warp >= 2) {
+                for (int b = 0; b < boxes; ++b) {
+                    uint32_t v[16];
+                    tc_ld_32x32b_x16(tlane + 16 * b, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (ok && 16 * b + j < tokens) finish<ACT>(p, f, t0 + 16 * b + j, __uint_as_float(v[j]), amax);
+                }
+            }
+        } else {
+            // Every CTA of the cluster is past its MMAs: the stages' memory takes the partial sums of the tokens
+            // that this CTA finishes, [CTA][token][feature].
+            const int mine = (tokens + splits - 1) / splits;
+            cluster_sync();
+            if (warp >= 2) {
+                const uint32_t col = sbase + 4 * ((warp & 3) * 32 + lane) + rank * mine * F_ROWS * 4;
+                for (int b = 0; b < boxes; ++b) {
+                    uint32_t v[16];
+                    tc_ld_32x32b_x16(tlane + 16 * b, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int t = 16 * b + j;
+                        if (t < tokens) {
+                            const int owner = t / mine;
+                            store_remote(col + (t - owner * mine) * F_ROWS * 4, owner, __uint_as_float(v[j]));
+                        }
+                    }
+                }
+            }
+            cluster_sync();
+            if (warp >= 2) {
+                const float* part = reinterpret_cast<const float*>(smem) + (warp & 3) * 32 + lane;
+                const int count = min(mine, tokens - rank * mine);
+                for (int t = 0; t < count; ++t) {
+                    float sum = 0.0f;
+                    for (int c = 0; c < splits; ++c) sum += part[(c * mine + t) * F_ROWS];
+                    if (ok) finish<ACT>(p, f, t0 + rank * mine + t, sum, amax);
+                }
+            }
+        }
+        if (t0 + TOK < stop) {      // the next pass writes the accumulator and the stages again
+            tc_fence_before();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (splits == 1) __syncthreads();
+            else cluster_sync();
+            tc_fence_after();
+        }
+    }
+    if (warp >= 2 && p.c_amax) {
+        __syncwarp();
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, amax);
+        if (lane == 0 && m) atomicMax(p.c_amax, m);
+    }
+    if (p.offsets && warp >= 2) {
+        // rows without a token: the segment's for these features, and those behind the last segment
+        const int esz = p.out_bf16 ? 2 : 4, worker = rank * 4 + warp - 2, all = gridDim.x * 4;
+        const int cols = min(F_ROWS, p.N - n0), end = max(segment_start(p.offsets, e + 1, p.M), stop);
+        uint8_t* c = static_cast<uint8_t*>(p.c) + (int64_t)n0 * esz;
+        zero_rows(c, (int64_t)cols * esz, p.ldc * esz, stop, end, worker, splits * 4, lane);
+        if (p.pre) zero_rows(p.pre + n0, cols * 2, p.ldp * 2, stop, end, worker, splits * 4, lane);
+        const int tail = segment_start(p.offsets, p.experts, p.M), me = blockIdx.x * 4 + warp - 2;
+        zero_rows(p.c, (int64_t)p.N * esz, p.ldc * esz, tail, p.M, me, all, lane);
+        if (p.pre) zero_rows(p.pre, (int64_t)p.N * 2, p.ldp * 2, tail, p.M, me, all, lane);
+    }
+    // after an abort too: no copy and no MMA in flight when memory is released
+    if (warp == 0 && lane == 0) {
+        for (int st = 0; st < L::kStages; ++st)
+            if (issued_any & (1u << st)) {
+                const unsigned long long w0 = globaltimer();
+                while (!mbar_try(bar_full + 8 * st, (issued_parity >> st) & 1u) && globaltimer() - w0 < kWaitLimitNs) {}
+            }
+    }
+    if (warp == 1 && lane == 0) {
+        tc_commit(bar_drain);
+        const unsigned long long w0 = globaltimer();
+        while (!mbar_try(bar_drain, 0) && globaltimer() - w0 < kWaitLimitNs) {}
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
+    }
+}
+
+typedef void (*FewKernel)(const CUtensorMap, const CUtensorMap, FewParams);
+
+template <int TOK>
+FewKernel few_kernel(int act) {
+    switch (act) {
+        case ACT_RELU: return gemm_few_kernel<TOK, ACT_RELU>;
+        case ACT_RELU2: return gemm_few_kernel<TOK, ACT_RELU2>;
+        case ACT_GELU: return gemm_few_kernel<TOK, ACT_GELU>;
+        case ACT_GELU_TANH: return gemm_few_kernel<TOK, ACT_GELU_TANH>;
+        case ACT_SILU: return gemm_few_kernel<TOK, ACT_SILU>;
+        default: return gemm_few_kernel<TOK, ACT_NONE>;
+    }
+}
+
+int prepared_sms() {
+    static int cached[64];
+    static std::mutex mu;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cached[dev]) {
+        int n = 0;
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        for (int act = 0; act < kNumActivations; ++act) {
+            cudaFuncSetAttribute(few_kernel<32>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<32>::kBytes);
+            cudaFuncSetAttribute(few_kernel<128>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kBytes);
+        }
+        cached[dev] = n > 0 ? n : 148;
+    }
+    return cached[dev];
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
+    const int sms = prepared_sms();
+    FewParams p{};
+    p.sfx = g.sfa;
+    p.sfw = g.sfb;
+    p.x_gs = g.a_gs;
+    p.w_gs = g.b_gs;
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.K = (int)g.K;
+    p.chunks_k = (int)mma_chunks_k(g.K);
+    p.tiles = (int)ceil_div(g.N, F_ROWS);
+    p.sfw_stride = (int64_t)mma_scale_bytes(g.N, g.K);
+    p.offsets = g.offsets;
+    p.counts = g.counts;
+    p.experts = g.offsets ? (int)g.experts : 1;
+    p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+    p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+    p.ldr = g.ldr;
+    p.out_bf16 = g.out_bf16;
+    p.c = g.c;
+    p.ldc = g.ldc;
+    p.pre = static_cast<__nv_bfloat16*>(g.pre);
+    p.ldp = g.ldp;
+    p.c_amax = reinterpret_cast<unsigned int*>(g.c_amax);
+    CUtensorMap mw, mx;
+    if (!make_code_map(&mw, g.b, p.experts * g.N, g.K, F_ROWS) || !make_code_map(&mx, g.a, g.M, g.K, 16))
+        return cudaErrorInvalidValue;
+    // The largest cluster whose CTAs are resident together (two to an SM) and have two blocks of K each.
+    const int64_t units = (int64_t)p.tiles * p.experts, blocks = ceil_div(g.K, 256);
+    int splits = 1;
+    while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
+    const bool small = !g.offsets && g.M <= 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.blockDim = dim3(F_THREADS);
+    cfg.dynamicSmemBytes = small ? Layout<32>::kBytes : Layout<128>::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, small ? few_kernel<32>(g.act) : few_kernel<128>(g.act), mw, mx, p);
+}
+
+unsigned int* few_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_error_word) == cudaSuccess ? static_cast<unsigned int*>(p) : nullptr;
+}
+
+}  // namespace nvfp4

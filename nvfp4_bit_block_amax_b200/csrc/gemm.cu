@@ -42,6 +42,7 @@
 #include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "segments.cuh"
 #include "tc.cuh"
 
 namespace nvfp4 {
@@ -652,24 +653,13 @@ __device__ __forceinline__ bool epilogue_half_pair(const KParams& p, int tile, i
 }
 
 // ------------------------------------------------- tiles of the pair kernel --
-// Expert segments.  offsets and counts are device data that nothing has
-// checked: wherever they are read they are clamped to 128-aligned ranges inside
-// [0, limit), and a tile whose rows would leave the operands is left out, so
-// that whatever they held, no access goes out of bounds.  ROWS also needs to
-// know which segment an M-tile lies in: a table in shared memory holds the
-// first M-tile of each expert, its last entry the number of M-tiles.
+// ROWS needs to know which segment an M-tile lies in: a table in shared memory
+// holds the first M-tile of each expert, its last entry the number of M-tiles.
 struct Groups {
     uint16_t* first;   // [experts + 1]
 };
 __device__ __forceinline__ Groups groups_at(uint8_t* smem) {
     return Groups{reinterpret_cast<uint16_t*>(smem + X_OFF_GROUPS)};
-}
-__device__ __forceinline__ int segment_start(const KParams& p, int e, int limit) {
-    return min(max(__ldg(p.offsets + e), 0), limit) & ~127;
-}
-__device__ __forceinline__ int segment_end(const KParams& p, int e, int limit) {
-    const int start = segment_start(p, e, limit);
-    return start + min(max(__ldg(p.counts + e), 0), max(segment_start(p, e + 1, limit) - start, 0));
 }
 // One warp fills the table (a running sum over lanes).
 __device__ __forceinline__ void fill_groups(const Groups& g, const KParams& p, int lane) {
@@ -677,7 +667,7 @@ __device__ __forceinline__ void fill_groups(const Groups& g, const KParams& p, i
     if (lane == 0) g.first[0] = 0;
     for (int base = 0; base < p.experts; base += 32) {
         const int i = base + lane;
-        const int n0 = i < p.experts ? segment_start(p, i + 1, p.M) - segment_start(p, i, p.M) : 0;
+        const int n0 = i < p.experts ? segment_start(p.offsets, i + 1, p.M) - segment_start(p.offsets, i, p.M) : 0;
         int n = (max(n0, 0) + 255) >> 8;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -718,10 +708,10 @@ __device__ __forceinline__ Tile tile_at(int t, const KParams& p, const Groups& g
             else hi = mid - 1;
         }
         r.e = lo;
-        r.m0 = segment_start(p, lo, p.M) + (tm - g.first[lo]) * 256;
+        r.m0 = segment_start(p.offsets, lo, p.M) + (tm - g.first[lo]) * 256;
         r.k0 = 0;
-        r.row_end = segment_start(p, lo + 1, p.M);
-        r.row_live = segment_end(p, lo, p.M);
+        r.row_end = segment_start(p.offsets, lo + 1, p.M);
+        r.row_live = segment_end(p.offsets, p.counts, lo, p.M);
         r.k_steps = p.K / 64;
         if (r.m0 >= r.row_end) {   // not from a sort's offsets: rows that exist, none stored
             r.m0 = 0;
@@ -732,9 +722,9 @@ __device__ __forceinline__ Tile tile_at(int t, const KParams& p, const Groups& g
         r.e = t / per;
         tile_coords(t - r.e * per, p, tm, tn);
         r.m0 = tm * 256;
-        const int start = segment_start(p, r.e, p.K);
+        const int start = segment_start(p.offsets, r.e, p.K);
         r.k0 = start >> 6;
-        r.k_steps = (segment_end(p, r.e, p.K) - start + 63) >> 6;
+        r.k_steps = (segment_end(p.offsets, p.counts, r.e, p.K) - start + 63) >> 6;
         r.row_end = r.row_live = p.M;
     } else {
         tile_coords(t, p, tm, tn);
@@ -760,21 +750,9 @@ __device__ __forceinline__ int tile_steps(int t, const KParams& p, Steps& seen) 
     const int e = t / (p.tiles_m * p.tiles_n);
     if (e != seen.e) {
         seen.e = e;
-        seen.n = (segment_end(p, e, p.K) - segment_start(p, e, p.K) + 63) >> 6;
+        seen.n = (segment_end(p.offsets, p.counts, e, p.K) - segment_start(p.offsets, e, p.K) + 63) >> 6;
     }
     return seen.n;
-}
-
-// The rows behind the last segment become zeros in C and pre; the epilogue
-// warps of the grid share them, before their first tile is ready.
-__device__ __forceinline__ void zero_rows(uint8_t* p, int64_t row_bytes, int64_t ld_bytes, int first, int last, int worker,
-                                          int workers, int lane) {
-    for (int64_t r = (int64_t)first + worker; r < last; r += workers) {
-        uint8_t* q = p + r * ld_bytes;   // 16-byte aligned
-        for (int64_t b = 16 * lane; b + 16 <= row_bytes; b += 512) *reinterpret_cast<uint4*>(q + b) = make_uint4(0, 0, 0, 0);
-        const int64_t b = row_bytes / 16 * 16 + 2 * lane;
-        if (b < row_bytes) *reinterpret_cast<uint16_t*>(q + b) = 0;
-    }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -1210,10 +1188,11 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         uint32_t amax_acc = 0;
         bool first = true;
         if constexpr (MODE == ROWS) {
-            const int begin = segment_start(p, p.experts, p.M), esz = p.out_bf16 ? 2 : 4;
+            const int begin = segment_start(p.offsets, p.experts, p.M), esz = p.out_bf16 ? 2 : 4;
             const int worker = blockIdx.x * EPI_WARPS + warp - kEpilogueWarp, workers = gridDim.x * EPI_WARPS;
-            zero_rows(static_cast<uint8_t*>(p.c), (int64_t)p.N * esz, p.ldc * esz, begin, p.M, worker, workers, lane);
-            if (p.pre) zero_rows(reinterpret_cast<uint8_t*>(p.pre), (int64_t)p.N * 2, p.ldp * 2, begin, p.M, worker, workers, lane);
+            // rows behind the last segment, before this warp's first tile is ready
+            zero_rows(p.c, (int64_t)p.N * esz, p.ldc * esz, begin, p.M, worker, workers, lane);
+            if (p.pre) zero_rows(p.pre, (int64_t)p.N * 2, p.ldp * 2, begin, p.M, worker, workers, lane);
         }
         for (int tile = cluster; tile < num_tiles; tile += n_clusters) {
             if constexpr (MODE == PLAIN) {
@@ -1256,11 +1235,13 @@ __global__ void wait_selftest_kernel(unsigned long long limit_ns) {
 }
 
 // ----------------------------------------------------------- host side -----
+}  // namespace
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn() {
+static EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -1284,6 +1265,8 @@ bool make_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t k,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // Boxes of 32 rows x width bytes (64 or 128), swizzled over that width.
 bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ldc, bool bf16, int width = 64) {
@@ -1486,12 +1469,23 @@ cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
 unsigned int read_and_clear_error_word(cudaStream_t s, cudaError_t* err) {
     *err = cudaStreamSynchronize(s);
     if (*err != cudaSuccess) return 0;
-    unsigned int w = 0;
-    *err = cudaMemcpyFromSymbol(&w, g_error_word, sizeof(w));
+    void* mine = nullptr;
+    *err = cudaGetSymbolAddress(&mine, g_error_word);
     if (*err != cudaSuccess) return 0;
-    const unsigned int zero = 0;
-    *err = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
-    return w;
+    unsigned int any = 0;
+    for (unsigned int* word : {static_cast<unsigned int*>(mine), few_error_word()}) {
+        if (!word) {
+            *err = cudaErrorInvalidSymbol;
+            return 0;
+        }
+        unsigned int w = 0;
+        *err = cudaMemcpy(&w, word, sizeof(w), cudaMemcpyDeviceToHost);
+        if (*err != cudaSuccess) return 0;
+        const unsigned int zero = 0;
+        *err = cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+        any |= w;
+    }
+    return any;
 }
 
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s) {

@@ -1,6 +1,7 @@
 // internal.h -- host-side launchers shared between the C-ABI layer and the kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -92,6 +93,10 @@ struct GemmExtArgs {
     int wgrad;
 };
 cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s);
+cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s);
+unsigned int* few_error_word();   // device address
+// Tensor map of a code matrix [rows x k/2 bytes]: boxes of box_rows x 128 bytes, 128-byte swizzle.
+bool make_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t k, int box_rows);
 constexpr int64_t kMaxExpertsArg = 512;
 constexpr int64_t kMaxSortedRows = 1 << 23;   // rows of a product over sorted rows: its tiles are counted in 16 bits
 
