@@ -13,9 +13,12 @@
 //     result every time.
 //   - Two CTAs to an SM, each with 72 KB (64 tokens and more: 54 KB) of weight
 //     in flight, several times what hides the latency of HBM.
-//   - Warp 0: TMA producer.  Warp 1: block scales to tensor memory (tcgen05.cp,
-//     which costs the tensor pipe little here) and the MMAs.  Warps 2 .. 5: the
-//     epilogue, a feature to a lane, a token to a column.
+//   - Warp 0: TMA producer.  Warp 1: the MMAs.  Warps 2 .. 5: block scales to
+//     tensor memory (a copy by the tensor core, tcgen05.cp, costs its pipe 64
+//     cycles; with 8 of them a block of K = 256 took 1015 cycles instead of
+//     the MMAs' 500, more than the time of its bytes), then the
+//     way out of tensor memory (a feature to a lane); all warps then finish
+//     rows, four features to a lane.
 // Every wait is bounded, as in the large product.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,12 +49,12 @@ struct Layout {
     static constexpr int kX = TOK * F_BKB;
     static constexpr int kStage = F_W_STAGE + kX + 2 * F_SF_STAGE;
     static constexpr int kOffX = F_W_STAGE, kOffSfw = kOffX + kX, kOffSfx = kOffSfw + F_SF_STAGE;
-    static constexpr int kOffBar = kStages * kStage;   // full, empty per stage; accumulator
-    static constexpr int kOffMisc = kOffBar + (2 * kStages + 2) * 8;
+    static constexpr int kOffBar = kStages * kStage;   // full, empty, scales per stage; accumulator, drain
+    static constexpr int kOffMisc = kOffBar + (3 * kStages + 2) * 8;
     static constexpr int kBytes = kOffMisc + 16 + 1008;
     static constexpr uint32_t kSf = TOK;               // first tensor-memory column of the scales, 32 per stage
     static_assert(kStage % 1024 == 0 && kSf + kStages * 32 <= F_TMEM, "layout");
-    static_assert((TOK + 8) * F_ROWS * 4 <= kOffBar, "partial sums of a cluster fit in the stages");
+    static_assert(TOK >= 8 && TOK * F_ROWS * 4 <= kOffBar, "partial sums of a cluster fit in the stages");
 };
 
 struct FewParams {
@@ -78,10 +81,19 @@ struct FewParams {
     int act;
 };
 
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t smem) {
-    // 32 rows x 16 bytes, contiguous, no swizzle (8-row groups 128 bytes apart), copied to all four lane quarters
-    const uint64_t desc = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1u << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// One thread issues the MMAs of the CTA, and little should stand between them:
+// the upper words of the descriptors are constants, the lower ones, which hold
+// address / 16, a base per stage plus constants.
+constexpr uint32_t kCodesLo = 1u << 16, kCodesHi = (1024u >> 4) | 1u << 14 | 2u << 29;   // as desc_sw128
+__device__ __forceinline__ uint64_t codes_desc(uint32_t at16) { return (uint64_t)kCodesHi << 32 | (kCodesLo + at16); }
+// The K steps of one stage; `at` is its address / 16, `sf` its scales' columns.
+template <int OFF_X>
+__device__ __forceinline__ void issue_steps(uint32_t tmem, uint32_t at, uint32_t sf, uint32_t idesc, int nk, bool add) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < nk)
+            tc_mma_nvf4(tmem, codes_desc(at + 2 * j), codes_desc(at + OFF_X / 16 + 2 * j), idesc, sf + 4 * j, sf + 16 + 4 * j,
+                        j > 0 || add, false);
 }
 __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -104,28 +116,70 @@ __device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, float
         : "memory");
 }
 
-// One element of C from its sum over K.
+// Four consecutive features of one token, from their sums over K.
 struct Finish {
     float2 alpha;
-    float bias;
-    int64_t n;      // feature
-    bool on;        // a feature that exists
+    float bias[4];
+    int64_t n;      // first feature
+    int count;      // how many of them exist
 };
-template <int ACT>
-__device__ __forceinline__ void finish(const FewParams& p, const Finish& f, int64_t row, float sum, uint32_t& amax) {
-    if (!f.on) return;
-    const float z = fmaf(sum * f.alpha.x, f.alpha.y, f.bias);
-    if (p.pre) p.pre[row * p.ldp + f.n] = __float2bfloat16_rn(z);
-    float v = act_value<ACT>(z);
-    if (p.residual) v += __bfloat162float(p.residual[row * p.ldr + f.n]);
-    if (p.out_bf16) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        static_cast<__nv_bfloat16*>(p.c)[row * p.ldc + f.n] = h;
-        v = __bfloat162float(h);
+__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* q, const uint2& w, int count) {
+    if (count >= 4) {
+        *reinterpret_cast<uint2*>(q) = w;
     } else {
-        static_cast<float*>(p.c)[row * p.ldc + f.n] = v;
+        const uint32_t h[2] = {w.x, w.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < count) reinterpret_cast<uint16_t*>(q)[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
     }
-    amax = max(amax, __float_as_uint(fabsf(v)));
+}
+template <int ACT>
+__device__ __forceinline__ void finish(const FewParams& p, const Finish& f, int64_t row, const float4& sum, uint32_t& amax) {
+    if (f.count <= 0) return;
+    float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e] * f.alpha.x, f.alpha.y, f.bias[e]);
+    if (p.pre) store4(p.pre + row * p.ldp + f.n, pack4(v), f.count);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = act_value<ACT>(v[e]);
+    if (p.residual) {
+        const __nv_bfloat16* r = p.residual + row * p.ldr + f.n;
+        if (f.count >= 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(r);
+            v[0] += bf16_lo(w.x);
+            v[1] += bf16_hi(w.x);
+            v[2] += bf16_lo(w.y);
+            v[3] += bf16_hi(w.y);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < f.count) v[e] += __bfloat162float(r[e]);
+        }
+    }
+    if (p.out_bf16) {
+        const uint2 w = pack4(v);
+        store4(static_cast<__nv_bfloat16*>(p.c) + row * p.ldc + f.n, w, f.count);
+        v[0] = bf16_lo(w.x);
+        v[1] = bf16_hi(w.x);
+        v[2] = bf16_lo(w.y);
+        v[3] = bf16_hi(w.y);
+    } else {
+        float* q = static_cast<float*>(p.c) + row * p.ldc + f.n;
+        if (f.count >= 4) {
+            *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < f.count) q[e] = v[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < f.count) amax = max(amax, __float_as_uint(fabsf(v[e])));
 }
 
 template <int TOK, int ACT>
@@ -136,7 +190,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + L::kOffBar, bar_empty = bar_full + 8 * L::kStages;
-    const uint32_t bar_acc = bar_empty + 8 * L::kStages, bar_drain = bar_acc + 8;
+    const uint32_t bar_sf = bar_empty + 8 * L::kStages, bar_acc = bar_sf + 8 * L::kStages, bar_drain = bar_acc + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
 
@@ -154,6 +208,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
+            mbar_init(bar_sf + 8 * s, 4);
         }
         mbar_init(bar_acc, 1);
         mbar_init(bar_drain, 1);
@@ -171,17 +226,19 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Finish f{};
-    if (warp >= 2) {
-        f.n = n0 + (warp & 3) * 32 + lane;
-        f.on = f.n < p.N;
+    Finish f;
+    {
+        f.n = n0 + 4 * lane;
+        f.count = (int)min((int64_t)4, p.N - f.n);
         const float sx = __ldg(p.x_gs), sw = __ldg(p.w_gs + e), a = __fmul_rn(sx, sw);
         // as the large product: one factor, or two where it leaves the normal range
         f.alpha = a >= 0x1p-126f && a <= 0x1.fffffep127f ? make_float2(a, 1.0f) : make_float2(sx, sw);
-        f.bias = p.bias && f.on ? __bfloat162float(p.bias[(int64_t)e * p.N + f.n]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.bias[i] = p.bias && i < f.count ? __bfloat162float(p.bias[(int64_t)e * p.N + f.n + i]) : 0.0f;
     }
     uint32_t amax = 0;
-    int s = 0;                      // stage and its phase, of the producer and of the MMA role
+    int s = 0;                      // stage and its phase, of each role
     uint32_t phase = 0, acc_phase = 0;
     uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
     bool ok = true;
@@ -211,70 +268,78 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 const uint32_t idesc =
                     (1u << 7) | (1u << 10) | ((uint32_t)(16 * boxes >> 3) << 17) | ((uint32_t)(F_ROWS >> 4) << 24);
                 for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                    if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
+                    // raised by the scale warps once the stage had landed
+                    if (!mbar_wait(bar_sf + 8 * s, phase, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const int nk = min(4, steps - kb * 4);
-                    const uint32_t at = sbase + s * L::kStage, sf = tmem + L::kSf + s * 32;
-                    for (int j = 0; j < nk; ++j) {
-                        cp_scales(sf + 4 * j, at + L::kOffSfw + 512 * j);
-                        cp_scales(sf + 16 + 4 * j, at + L::kOffSfx + 512 * j);
-                    }
-                    for (int j = 0; j < nk; ++j)
-                        tc_mma_nvf4(tmem, desc_sw128(at + j * 32), desc_sw128(at + L::kOffX + j * 32), idesc, sf + 4 * j,
-                                    sf + 16 + 4 * j, kb > kb0 || j > 0, false);
+                    issue_steps<L::kOffX>(tmem, (sbase + s * L::kStage) >> 4, tmem + L::kSf + s * 32, idesc,
+                                          min(4, steps - kb * 4), kb > kb0);
                     tc_commit(bar_empty + 8 * s);
                     if (++s == L::kStages) { s = 0; phase ^= 1; }
                 }
                 tc_commit(bar_acc);
             }
         } else {
-            ok = mbar_wait(bar_acc, acc_phase, abort_flag) && ok;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
+                const uint32_t sf = sbase + s * L::kStage + L::kOffSfw + 16 * lane;
+                uint32_t w[16], x[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 a = lds128(sf + 512 * j), b = lds128(sf + F_SF_STAGE + 512 * j);
+                    w[4 * j] = a.x; w[4 * j + 1] = a.y; w[4 * j + 2] = a.z; w[4 * j + 3] = a.w;
+                    x[4 * j] = b.x; x[4 * j + 1] = b.y; x[4 * j + 2] = b.z; x[4 * j + 3] = b.w;
+                }
+                tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32, w);
+                tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32 + 16, x);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sf + 8 * s);
+                if (++s == L::kStages) { s = 0; phase ^= 1; }
+            }
+            (void)mbar_wait(bar_acc, acc_phase, abort_flag);   // run out: the results are wrong and the error word says so
             tc_fence_after();
         }
         acc_phase ^= 1;
         __syncwarp();
-        const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        if (splits == 1) {
-            if (warp >= 2) {
-                for (int b = 0; b < boxes; ++b) {
-                    uint32_t v[16];
-                    tc_ld_32x32b_x16(tlane + 16 * b, v);
-                    tc_wait_ld();
+        // The stages' memory takes the partial sums, [CTA][token][feature], of the tokens that a CTA finishes: all
+        // of them, or in a cluster a share.  Every MMA that reads a stage has to be done for that, in all its CTAs.
+        int shift = 0;              // a share is 2^shift tokens
+        while ((splits << shift) < tokens) ++shift;
+        if (splits > 1) cluster_sync();
+        if (warp >= 2) {
+            const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t col = sbase + 4 * ((warp & 3) * 32 + lane) + (rank << shift) * F_ROWS * 4;
+            for (int b = 0; b < boxes; ++b) {
+                uint32_t v[16];
+                tc_ld_32x32b_x16(tlane + 16 * b, v);
+                tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (ok && 16 * b + j < tokens) finish<ACT>(p, f, t0 + 16 * b + j, __uint_as_float(v[j]), amax);
+                for (int j = 0; j < 16; ++j) {
+                    const int t = 16 * b + j;
+                    if (t >= tokens) break;
+                    const uint32_t at = col + (t & ((1 << shift) - 1)) * F_ROWS * 4;
+                    if (splits > 1) store_remote(at, t >> shift, __uint_as_float(v[j]));
+                    else asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v[j]) : "memory");
                 }
             }
-        } else {
-            // Every CTA of the cluster is past its MMAs: the stages' memory takes the partial sums of the tokens
-            // that this CTA finishes, [CTA][token][feature].
-            const int mine = (tokens + splits - 1) / splits;
-            cluster_sync();
-            if (warp >= 2) {
-                const uint32_t col = sbase + 4 * ((warp & 3) * 32 + lane) + rank * mine * F_ROWS * 4;
-                for (int b = 0; b < boxes; ++b) {
-                    uint32_t v[16];
-                    tc_ld_32x32b_x16(tlane + 16 * b, v);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int t = 16 * b + j;
-                        if (t < tokens) {
-                            const int owner = t / mine;
-                            store_remote(col + (t - owner * mine) * F_ROWS * 4, owner, __uint_as_float(v[j]));
-                        }
-                    }
+        }
+        if (splits > 1) cluster_sync();
+        else __syncthreads();
+        {
+            const float4* part = reinterpret_cast<const float4*>(smem) + lane;
+            const int first = rank << shift, count = min(1 << shift, tokens - first);
+            for (int t = warp; t < count; t += F_THREADS / 32) {
+                float4 sum = part[t * (F_ROWS / 4)];
+                for (int c = 1; c < splits; ++c) {
+                    const float4 q = part[((c << shift) + t) * (F_ROWS / 4)];
+                    sum.x += q.x;
+                    sum.y += q.y;
+                    sum.z += q.z;
+                    sum.w += q.w;
                 }
-            }
-            cluster_sync();
-            if (warp >= 2) {
-                const float* part = reinterpret_cast<const float*>(smem) + (warp & 3) * 32 + lane;
-                const int count = min(mine, tokens - rank * mine);
-                for (int t = 0; t < count; ++t) {
-                    float sum = 0.0f;
-                    for (int c = 0; c < splits; ++c) sum += part[(c * mine + t) * F_ROWS];
-                    if (ok) finish<ACT>(p, f, t0 + rank * mine + t, sum, amax);
-                }
+                finish<ACT>(p, f, t0 + first + t, sum, amax);
             }
         }
         if (t0 + TOK < stop) {      // the next pass writes the accumulator and the stages again
@@ -285,7 +350,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             tc_fence_after();
         }
     }
-    if (warp >= 2 && p.c_amax) {
+    if (p.c_amax) {
         __syncwarp();
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, amax);
         if (lane == 0 && m) atomicMax(p.c_amax, m);
