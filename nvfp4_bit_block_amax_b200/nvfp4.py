@@ -141,8 +141,8 @@ def _p(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream's handle, without building a Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -503,35 +503,41 @@ def quantize_dual(x: torch.Tensor, rounding: int = NVFP4_RNE, sr_seed: int = 0, 
 # ------------------------------------------------------ the linear layer ----
 def _matrix(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> int:
     """Row stride of a [rows x cols] matrix with unit column stride (checked)."""
-    assert t.dtype == dtype and t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1)
-    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    assert t.dtype is dtype and t.shape == (rows, cols)
+    ld, unit = t.stride()
+    assert unit == 1 or cols == 1
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _padded(rows: int, cols: int, dtype, device) -> torch.Tensor:
     """A [rows x cols] view whose row stride is a multiple of 8 elements."""
     ld = (cols + 7) // 8 * 8
-    t = torch.empty(rows, ld, dtype=dtype, device=device)
+    t = torch.empty((rows, ld), dtype=dtype, device=device)
     return t if ld == cols else t[:, :cols]
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     """Device scratch of one call: not reused before that call's stream is past it."""
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+    return _kept(ws, stream)
+
+
+def _kept(t: torch.Tensor, stream) -> torch.Tensor:
+    """t, allocated on the current stream and used on `stream`."""
     if stream is not None:
-        ws.record_stream(stream)
-    return ws
+        t.record_stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+    return t
 
 
 def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
-    assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.numel() == experts * rows * (k // 2)
-    assert scales_mma.is_contiguous() and scales_mma.numel() >= experts * nvfp4_mma_scale_bytes(rows, k)
-    assert gs.dtype == torch.float32 and gs.is_contiguous() and gs.numel() == experts
+    assert codes.dtype is torch.uint8 and codes.numel() == experts * rows * (k // 2) and codes.is_contiguous()
+    need = (rows + 127) // 128 * ((k // 16 + 3) // 4) * 512      # nvfp4_mma_scale_bytes
+    assert scales_mma.numel() >= experts * need and scales_mma.is_contiguous()
+    assert gs.dtype is torch.float32 and gs.numel() == experts and gs.is_contiguous()
 
 
 def _check_word(t):
-    assert t is None or (t.dtype == torch.float32 and t.numel() == 1)
+    assert t is None or (t.dtype is torch.float32 and t.numel() == 1)
 
 
 def gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: int, K: int, bias=None,
@@ -606,41 +612,26 @@ class MoePlan:
 
     def __post_init__(self):
         for t in (self.offsets, self.counts, self.row_copy, self.copy_row):
-            assert t.dtype == torch.int32 and t.is_contiguous()
-        assert self.offsets.numel() == self.counts.numel() + 1 and self.copy_row.dim() == 2
-
-    @property
-    def experts(self) -> int:
-        return self.counts.numel()
-
-    @property
-    def rows(self) -> int:
-        return self.row_copy.numel()
-
-    @property
-    def tokens(self) -> int:
-        return self.copy_row.shape[0]
-
-    @property
-    def topk(self) -> int:
-        return self.copy_row.shape[1]
+            assert t.dtype is torch.int32 and t.is_contiguous()
+        self.experts = self.counts.numel()
+        self.rows = self.row_copy.numel()
+        assert self.offsets.numel() == self.experts + 1
+        self.tokens, self.topk = self.copy_row.shape
 
 
 def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None, stream=None) -> MoePlan:
     """Sort the copies of int32 expert_ids [tokens x topk] by expert.  rows (default: enough for every routing)
     bounds the sorted matrices; copies that find no row are dropped."""
-    assert expert_ids.dtype == torch.int32 and expert_ids.dim() == 2 and expert_ids.is_contiguous()
-    n, dev = expert_ids.numel(), expert_ids.device
+    assert expert_ids.dtype is torch.int32 and expert_ids.dim() == 2 and expert_ids.is_contiguous()
+    n = expert_ids.numel()
     if rows is None:
         rows = nvfp4_moe_rows(n, experts)
-    plan = MoePlan(torch.empty(experts + 1, dtype=torch.int32, device=dev),
-                   torch.empty(experts, dtype=torch.int32, device=dev),
-                   torch.empty(rows, dtype=torch.int32, device=dev),
-                   torch.empty(expert_ids.shape, dtype=torch.int32, device=dev))
-    ws = _scratch(nvfp4_moe_workspace_size(n, experts), dev, stream)
-    nvfp4_moe_sort(expert_ids, n, experts, rows, plan.offsets, plan.counts, plan.row_copy, plan.copy_row, ws,
-                   ws.numel(), stream)
-    return plan
+    ws_bytes = nvfp4_moe_workspace_size(n, experts)
+    # one allocation: the call's scratch, then the plan's four arrays
+    buf = _kept(torch.empty(ws_bytes // 4 + 2 * experts + 1 + rows + n, dtype=torch.int32, device=expert_ids.device), stream)
+    ws, offsets, counts, row_copy, copy_row = buf.split((ws_bytes // 4, experts + 1, experts, rows, n))
+    nvfp4_moe_sort(expert_ids, n, experts, rows, offsets, counts, row_copy, copy_row, ws, ws_bytes, stream)
+    return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))
 
 
 def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = None,
