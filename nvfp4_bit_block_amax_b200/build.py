@@ -30,7 +30,7 @@ UNITS = {
     "layer.cu": [],
     "api.cu": [],
 }
-HEADERS = ["activation.cuh", "common.cuh", "internal.h", "segments.cuh", "tc.cuh"]
+HEADERS = ["activation.cuh", "common.cuh", "internal.h", "launch.cuh", "segments.cuh", "tc.cuh"]
 
 
 def _nvcc() -> str:

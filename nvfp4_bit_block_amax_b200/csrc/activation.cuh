@@ -132,4 +132,35 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
     } else return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
 }
 
+// act_grad_value of two values at once.
+template <int ACT>
+__device__ __forceinline__ float2 act_grad_value2(float2 g, float2 z) {
+    if constexpr (ACT == ACT_SILU || ACT == ACT_GELU_TANH) {
+        float2 x = z, dx = both(1.0f);   // s(x); slope s + z s (1 - s) x'
+        if constexpr (ACT == ACT_GELU_TANH) {
+            const float2 zz = __fmul2_rn(z, z);
+            x = __fmul2_rn(z, __ffma2_rn(zz, both(kTanhScale2 * kTanhCubic), both(kTanhScale2)));
+            dx = __ffma2_rn(zz, both(3.0f * kTanhScale2 * kTanhCubic), both(kTanhScale2));
+        }
+        const float2 s = logistic2(__fmul2_rn(x, both(-kLog2e)));
+        const float2 d = __fmul2_rn(s, __ffma2_rn(s, both(-1.0f), both(1.0f)));   // 0 far out, where z x' may overflow
+        const float2 q = __fmul2_rn(z, dx);
+        return __fmul2_rn(g, make_float2(d.x == 0.0f ? s.x : fmaf(d.x, q.x, s.x), d.y == 0.0f ? s.y : fmaf(d.y, q.y, s.y)));
+    } else if constexpr (ACT == ACT_GELU) {
+        const float2 e = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
+        const float2 density = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+        const float2 t0 = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(kHastingsP), both(1.0f));
+        const float2 t = make_float2(rcp_fast(t0.x), rcp_fast(t0.y));
+        float2 poly = __ffma2_rn(t, both(0.5f * kHastings5), both(0.5f * kHastings4));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings3));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings2));
+        poly = __ffma2_rn(t, poly, both(0.5f * kHastings1));
+        const float2 tail = __fmul2_rn(__fmul2_rn(t, poly), density);
+        const float2 cdf = make_float2(z.x > 0.0f ? 1.0f - tail.x : tail.x, z.y > 0.0f ? 1.0f - tail.y : tail.y);
+        const float2 q = __fmul2_rn(z, both(0.3989422804f));
+        return __fmul2_rn(g, make_float2(density.x == 0.0f ? cdf.x : fmaf(density.x, q.x, cdf.x),
+                                         density.y == 0.0f ? cdf.y : fmaf(density.y, q.y, cdf.y)));
+    } else return make_float2(act_grad_value<ACT>(g.x, z.x), act_grad_value<ACT>(g.y, z.y));
+}
+
 }  // namespace nvfp4

@@ -388,12 +388,10 @@ static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
         (g.pre && (!aligned16(g.pre) || g.ldp % 8)))
         return NVFP4_ERR_MISALIGNED;
     g.out_bf16 = out_dtype == NVFP4_OUT_BF16;
-    if (g.c_amax &&
-        cudaMemsetAsync(g.c_amax, 0, sizeof(float), static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return NVFP4_ERR_CUDA;
+    if (zero_word(g.c_amax, static_cast<cudaStream_t>(stream)) != cudaSuccess) return NVFP4_ERR_CUDA;
     const bool few = !g.wgrad && (g.experts ? g.M <= 128 * (g.experts + 1) : g.M <= 128);
     cudaError_t e = (few ? launch_gemm_few : launch_gemm_ext)(g, static_cast<cudaStream_t>(stream));
-    g_launches += 1;
+    g_launches += g.c_amax ? 2 : 1;
     return from_cuda(e);
 }
 
@@ -466,7 +464,7 @@ nvfp4_status nvfp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8_t* a_s
 }
 
 size_t nvfp4_act_grad_workspace_size(int64_t M, int64_t N) {
-    return M < 1 || N < 1 ? 0 : (size_t)(ceil_div(M, 128) * N) * sizeof(float);
+    return M < 1 || N < 1 || M >= kMaxDim || N >= kMaxDim ? 0 : act_grad_workspace(M, N);
 }
 
 nvfp4_status nvfp4_act_grad(const void* dy, int64_t ldy, const void* z, int64_t ldz, int64_t M, int64_t N,

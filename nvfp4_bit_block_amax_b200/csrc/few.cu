@@ -28,6 +28,7 @@
 #include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "segments.cuh"
 #include "tc.cuh"
 
@@ -193,13 +194,12 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const uint32_t bar_sf = bar_empty + 8 * L::kStages, bar_acc = bar_sf + 8 * L::kStages, bar_drain = bar_acc + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+    unsigned int* s_amax = reinterpret_cast<unsigned int*>(smem + L::kOffMisc + 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), splits = (int)cluster_size();
     const int unit = blockIdx.x / splits;
     const int e = unit / p.tiles, tile = unit - e * p.tiles;
-    const int start = p.offsets ? segment_start(p.offsets, e, p.M) : 0;
-    const int stop = p.offsets ? segment_end(p.offsets, p.counts, e, p.M) : p.M;
     const int n0 = tile * F_ROWS;
     const int steps = p.K / 64, blocks = (steps + 3) / 4;
     const int kb0 = (int)((int64_t)blocks * rank / splits), kb1 = (int)((int64_t)blocks * (rank + 1) / splits);
@@ -213,6 +213,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         mbar_init(bar_acc, 1);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
+        *s_amax = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -221,6 +222,9 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                      "r"(F_TMEM));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    wait_for_stream();
+    const int start = p.offsets ? segment_start(p.offsets, e, p.M) : 0;
+    const int stop = p.offsets ? segment_end(p.offsets, p.counts, e, p.M) : p.M;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -350,10 +354,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             tc_fence_after();
         }
     }
-    if (p.c_amax) {
+    if (p.c_amax) {                 // over the CTA, then one atomic
         __syncwarp();
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, amax);
-        if (lane == 0 && m) atomicMax(p.c_amax, m);
+        if (lane == 0 && m) atomicMax(s_amax, m);
     }
     if (p.offsets && warp >= 2) {
         // rows without a token: the segment's for these features, and those behind the last segment
@@ -366,21 +370,26 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         zero_rows(p.c, (int64_t)p.N * esz, p.ldc * esz, tail, p.M, me, all, lane);
         if (p.pre) zero_rows(p.pre, (int64_t)p.N * 2, p.ldp * 2, tail, p.M, me, all, lane);
     }
-    // after an abort too: no copy and no MMA in flight when memory is released
-    if (warp == 0 && lane == 0) {
-        for (int st = 0; st < L::kStages; ++st)
-            if (issued_any & (1u << st)) {
-                const unsigned long long w0 = globaltimer();
-                while (!mbar_try(bar_full + 8 * st, (issued_parity >> st) & 1u) && globaltimer() - w0 < kWaitLimitNs) {}
-            }
-    }
-    if (warp == 1 && lane == 0) {
-        tc_commit(bar_drain);
-        const unsigned long long w0 = globaltimer();
-        while (!mbar_try(bar_drain, 0) && globaltimer() - w0 < kWaitLimitNs) {}
+    // After an abort, no copy and no MMA may be in flight when memory is released; otherwise every copy was waited for by
+    // the scale warps and every MMA by the accumulator's barrier.
+    if (*abort_flag) {
+        if (warp == 0 && lane == 0) {
+            for (int st = 0; st < L::kStages; ++st)
+                if (issued_any & (1u << st)) {
+                    const unsigned long long w0 = globaltimer();
+                    while (!mbar_try(bar_full + 8 * st, (issued_parity >> st) & 1u) && globaltimer() - w0 < kWaitLimitNs) {}
+                }
+        }
+        if (warp == 1 && lane == 0) {
+            tc_commit(bar_drain);
+            const unsigned long long w0 = globaltimer();
+            while (!mbar_try(bar_drain, 0) && globaltimer() - w0 < kWaitLimitNs) {}
+        }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    if (p.c_amax && threadIdx.x == 0 && *s_amax) atomicMax(p.c_amax, *s_amax);
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
@@ -455,19 +464,8 @@ cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
     int splits = 1;
     while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
     const bool small = !g.offsets && g.M <= 32;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * splits));
-    cfg.blockDim = dim3(F_THREADS);
-    cfg.dynamicSmemBytes = small ? Layout<32>::kBytes : Layout<128>::kBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, small ? few_kernel<32>(g.act) : few_kernel<128>(g.act), mw, mx, p);
+    return launch_early(small ? few_kernel<32>(g.act) : few_kernel<128>(g.act), (unsigned)(units * splits), F_THREADS,
+                        small ? Layout<32>::kBytes : Layout<128>::kBytes, s, splits, mw, mx, p);
 }
 
 unsigned int* few_error_word() {

@@ -42,6 +42,7 @@
 #include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "segments.cuh"
 #include "tc.cuh"
 
@@ -1009,6 +1010,7 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
     const uint32_t bar_drain = bar_tempty + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P_OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P_OFF_MISC + 4);
+    unsigned int* s_amax = reinterpret_cast<unsigned int*>(smem + P_OFF_MISC + 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kScaleWarp = MODE == PLAIN ? 2 : 4, kEpilogueWarp = MODE == PLAIN ? 6 : 8;   // the first of each
@@ -1026,15 +1028,17 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         mbar_init(bar_tempty, 2 * EPI_WARPS);        // epilogue warps of both CTAs
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
+        *s_amax = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (MODE == ROWS && warp == kScaleWarp) fill_groups(groups, p, lane);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
+    if constexpr (MODE != PLAIN) wait_for_stream();
+    if (MODE == ROWS && warp == kScaleWarp) fill_groups(groups, p, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -1206,11 +1210,16 @@ gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_co
         }
         if (lane == 0) bulk_wait0();    // every store of this warp has completed
         __syncwarp();
-        if (p.c_amax) amax_publish(p.c_amax, amax_acc);
+        if (p.c_amax) {
+            // beyond PLAIN over the CTA first: a thousand warps that end together would queue at one address
+            if constexpr (MODE == PLAIN) amax_publish(p.c_amax, amax_acc);
+            else amax_publish(s_amax, amax_acc);
+        }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (MODE != PLAIN && p.c_amax && threadIdx.x == 0 && *s_amax) atomicMax(p.c_amax, *s_amax);
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
@@ -1359,23 +1368,6 @@ int group_for(int64_t rows_per_tile, int64_t K, int tiles_m) {
     return (int)gm;
 }
 
-cudaError_t launch_pairs(PairKernel kernel, int clusters, int threads, int smem, cudaStream_t s, const CUtensorMap& ma,
-                         const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mp, const KParams& p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, mp, p);
-}
-
 }  // namespace
 
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
@@ -1420,8 +1412,20 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
     p.group_m = group_for(256, g.K, p.tiles_m);
     const int tiles = p.tiles_m * p.tiles_n;
     const int clusters = tiles < dev.pair_clusters ? tiles : dev.pair_clusters;
-    return p.mx ? launch_pairs(gemm_nvf4_pair_kernel<true, PLAIN>, clusters, P_NUM_THREADS, P_SMEM_BYTES, s, ma, mb, mc, mc, p)
-                : launch_pairs(gemm_nvf4_pair_kernel<false, PLAIN>, clusters, P_NUM_THREADS, P_SMEM_BYTES, s, ma, mb, mc, mc, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters);
+    cfg.blockDim = dim3(P_NUM_THREADS);
+    cfg.dynamicSmemBytes = P_SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return p.mx ? cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<true, PLAIN>, ma, mb, mc, mc, p)
+                : cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<false, PLAIN>, ma, mb, mc, mc, p);
 }
 
 cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
@@ -1463,7 +1467,7 @@ cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s) {
     const int64_t tiles = (rows ? ceil_div(g.M, 128) : p.tiles_m) * p.tiles_n * (g.wgrad ? g.experts : 1);
     const int clusters = (int)(tiles < dev.pair_clusters ? tiles : dev.pair_clusters);
     PairKernel kernel = ext_kernel(g.wgrad ? KSEG : rows ? ROWS : EPILOGUE, g.act);
-    return launch_pairs(kernel, clusters, X_NUM_THREADS, X_SMEM_BYTES, s, ma, mb, mc, mp, p);
+    return launch_early(kernel, 2 * clusters, X_NUM_THREADS, X_SMEM_BYTES, s, 2, ma, mb, mc, mp, p);
 }
 
 unsigned int read_and_clear_error_word(cudaStream_t s, cudaError_t* err) {

@@ -93,6 +93,7 @@ struct GemmExtArgs {
     int wgrad;
 };
 cudaError_t launch_gemm_ext(const GemmExtArgs& g, cudaStream_t s);
+cudaError_t zero_word(float* amax, cudaStream_t s);   // one launch; nothing for a null pointer
 cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s);
 unsigned int* few_error_word();   // device address
 // Tensor map of a code matrix [rows x k/2 bytes]: boxes of box_rows x 128 bytes, 128-byte swizzle.
@@ -114,8 +115,9 @@ struct ActGradArgs {
     int64_t lddz;
     float* dbias;                 // nullable
     float* amax;                  // nullable
-    float* workspace;             // [ceil(M / 128) x N], with dbias
+    float* workspace;             // act_grad_workspace(M, N) bytes, with dbias
 };
+size_t act_grad_workspace(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches);
 
 struct SortArgs {

@@ -16,6 +16,7 @@
 #include "activation.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace nvfp4 {
 
@@ -66,12 +67,16 @@ __device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
 }
 
 // ------------------------------------------------------ activation gradient --
-// dz = dy * act'(z) and the column sums of dz.  A CTA takes 128 rows x 256
-// columns (128 rows: no tile crosses an expert's segment), a warp 16 of the
-// rows, a lane 8 columns.  6 bytes per element moved; the sums of the 128
-// rows go to the workspace, [row tiles x N] binary32 (1/64 of the bytes), and
-// bias_grad_kernel adds them up in order.
-constexpr int kRowTile = 128, kColTile = 256;
+// dz = dy * act'(z) and the column sums of dz.  A CTA takes 128 (or 32) rows x
+// 256 columns, and since segments start at multiples of 128 no tile crosses
+// one; a warp takes every 8th of the rows, a lane 8 columns.  6 bytes per
+// element moved; the sums of a tile's rows go to the workspace, [row tiles x N]
+// binary32 (1/64 of the bytes with 128 rows), and bias_grad_kernel adds them
+// up in order.  With 128 rows a thread goes through its rows in four steps of
+// four; where that leaves fewer than 4 CTAs to an SM, 32 rows give every
+// thread one step: 1000 x 4100 16.4 -> 12.3 us.
+constexpr int kColTile = 256;
+constexpr int64_t kRowTile = 128, kRowTileFew = 32;
 
 struct ActGradParams {
     const __nv_bfloat16* dy;
@@ -80,6 +85,7 @@ struct ActGradParams {
     int64_t ldy, ldz, lddz;
     int64_t M, N;
     int64_t strips;        // ceil(N / kColTile)
+    int tile_rows;
     const int* offsets;    // nullable: rows in expert segments
     const int* counts;
     int experts;
@@ -106,10 +112,11 @@ __device__ __forceinline__ int64_t live_rows(const int* offsets, const int* coun
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
     __shared__ float s_sum[kWarps][kColTile];
+    wait_for_stream();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tile = blockIdx.x / p.strips, strip = blockIdx.x - tile * p.strips;   // columns fastest
-    const int64_t m0 = tile * kRowTile, col = strip * kColTile + 8 * lane;
-    const int64_t stop = min(m0 + kRowTile, p.M);                                // rows to write
+    const int64_t m0 = tile * p.tile_rows, col = strip * kColTile + 8 * lane;
+    const int64_t stop = min(m0 + p.tile_rows, p.M);                               // rows to write
     const int64_t live = min(live_rows(p.offsets, p.counts, p.experts, m0, p.M), stop);   // rows to compute
     const int64_t n = p.N - col;
     float sum[8] = {};
@@ -135,10 +142,12 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
                 unpack8(g[u], a);
                 unpack8(z[u], b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    a[e] = act_grad_value<ACT>(a[e], b[e]);
-                    if (r >= live) a[e] = 0.0f;
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 v = act_grad_value2<ACT>(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+                    a[e] = r < live ? v.x : 0.0f;
+                    a[e + 1] = r < live ? v.y : 0.0f;
                     sum[e] += a[e];
+                    sum[e + 1] += a[e + 1];
                 }
                 const uint4 o = pack8(a);
                 peak = absmax8(peak, o);
@@ -181,17 +190,18 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
 // dbias [experts x N] from the sums of the row tiles: 64 columns per CTA, the
 // tiles of a segment dealt to 4 threads per column, then added in order.
 __global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __restrict__ sums, int64_t M, int64_t N,
-                                                             const int* offsets, const int* counts, float* dbias) {
+                                                             int tile_rows, const int* offsets, const int* counts, float* dbias) {
     __shared__ float s[4][64];
+    wait_for_stream();
     const int e = blockIdx.y, part = threadIdx.x >> 6, c = threadIdx.x & 63;
     const int64_t col = (int64_t)blockIdx.x * 64 + c;
-    const int64_t tiles = (M + kRowTile - 1) / kRowTile;
+    const int64_t tiles = (M + tile_rows - 1) / tile_rows;
     int64_t first = 0, last = tiles;
     if (offsets) {
         const int64_t o = __ldg(offsets + e);
         const int64_t end = min(o + __ldg(counts + e), (int64_t)__ldg(offsets + e + 1));
-        first = max(o, (int64_t)0) / kRowTile;
-        last = min(tiles, (end + kRowTile - 1) / kRowTile);
+        first = max(o, (int64_t)0) / tile_rows;
+        last = min(tiles, (end + tile_rows - 1) / tile_rows);
     }
     float t = 0.0f;
     if (col < N) {
@@ -221,6 +231,7 @@ struct SortParams {
 
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(SortParams p) {
     extern __shared__ int s_count[];
+    wait_for_stream();
     for (int e = threadIdx.x; e < p.experts; e += kThreads) s_count[e] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.n);
@@ -242,6 +253,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(SortParams p) {
     for (int i = threadIdx.x; i < kWarps * p.experts; i += kThreads) s_at[i] = 0;
     if (threadIdx.x == 0) s_carry = 0;
     __syncthreads();
+    wait_for_stream();
     // this CTA's copies, counted per warp
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.n);
     const int part = p.chunk / kWarps;
@@ -345,15 +357,17 @@ __device__ __forceinline__ int row_of(const MoveParams& p, int64_t copy) {
     return r >= 0 && r < p.rows ? r : -1;
 }
 
-// Rows that hold no copy become zeros: one warp looks at 32 rows x 1024 columns.
+// Rows that hold no copy become zeros: one warp looks at 8 rows x 1024 columns
+// (few, because padding rows lie together: up to 127 behind each segment).
+constexpr int kZeroRows = 8;
 __device__ __forceinline__ int64_t zero_units(const MoveParams& p) {
-    return (p.rows + 31) / 32 * ((p.cols + 1023) / 1024);
+    return (p.rows + kZeroRows - 1) / kZeroRows * ((p.cols + 1023) / 1024);
 }
 __device__ __forceinline__ void zero_unit(const MoveParams& p, int64_t unit, int lane) {
-    const int64_t groups = (p.rows + 31) / 32;
-    const int64_t r0 = unit % groups * 32, c0 = unit / groups * 1024;
+    const int64_t groups = (p.rows + kZeroRows - 1) / kZeroRows;
+    const int64_t r0 = unit % groups * kZeroRows, c0 = unit / groups * 1024;
     bool empty = false;
-    if (r0 + lane < p.rows) {
+    if (lane < kZeroRows && r0 + lane < p.rows) {
         const int c = __ldg(p.row_copy + r0 + lane);
         empty = c < 0 || c >= p.tokens * p.topk;
     }
@@ -372,6 +386,7 @@ __device__ __forceinline__ void zero_unit(const MoveParams& p, int64_t unit, int
 // Sorted rows from token rows.  A warp takes 1024 columns of one token: reads
 // them once, 4 loads in flight per lane, and writes them topk times.
 __global__ void __launch_bounds__(kThreads) gather_kernel(MoveParams p) {
+    wait_for_stream();
     const int lane = threadIdx.x & 31;
     const int64_t segs = (p.cols + 1023) / 1024, units = p.tokens * segs, all = units + zero_units(p);
     uint32_t peak = 0;
@@ -403,33 +418,41 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(MoveParams p) {
 }
 
 // Token rows from sorted rows: a warp takes 512 columns of one token, the rows
-// of 4 copies in flight at a time, and sums in the order of the copies.
+// of 2 copies in flight at a time, and sums in the order of the copies.
+// 16384 x 2 x 8192 with the residual (VECS, COPIES): (2, 2) 0.162 ms, (4, 2)
+// 0.161, (2, 4) 0.197, (1, 2) 0.201, (1, 4) 0.269; of (2, 2) and (4, 2) the one
+// with more units for few tokens.
+constexpr int VECS = 2, COPIES = 2;
 __global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
+    wait_for_stream();
     const int lane = threadIdx.x & 31;
-    const int64_t segs = (p.cols + 511) / 512, units = p.tokens * segs;
+    constexpr int kCols = 256 * VECS;
+    const int64_t segs = (p.cols + kCols - 1) / kCols, units = p.tokens * segs;
     for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = u / segs, c0 = (u - t * segs) * 512 + 8 * lane;
-        const bool in[2] = {c0 < p.cols, c0 + 256 < p.cols};
-        float acc[2][8] = {};
-        uint4 res[2];
+        const int64_t t = u / segs, c0 = (u - t * segs) * kCols + 8 * lane;
+        bool in[VECS];
+        float acc[VECS][8] = {};
+        uint4 res[VECS];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < VECS; ++i) {
+            in[i] = c0 + 256 * i < p.cols;
             res[i] = p.other && in[i] ? ld_stream(p.other + t * p.ldo + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
-        for (int j0 = 0; j0 < p.topk; j0 += 4) {
-            uint4 v[4][2];
-            float w[4];
+        }
+        for (int j0 = 0; j0 < p.topk; j0 += COPIES) {
+            uint4 v[COPIES][VECS];
+            float w[COPIES];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < COPIES; ++j) {
                 const int r = j0 + j < p.topk ? row_of(p, t * p.topk + j0 + j) : -1;
                 w[j] = r < 0 ? 0.0f : p.weights ? __ldg(p.weights + t * p.topk + j0 + j) : 1.0f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < VECS; ++i)
                     v[j][i] = r >= 0 && in[i] ? ldg_stream(p.src + r * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < COPIES; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < VECS; ++i) {
                     float f[8];
                     unpack8(v[j][i], f);
 #pragma unroll
@@ -437,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
                 }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < VECS; ++i) {
             if (!in[i]) continue;
             float f[8];
             unpack8(res[i], f);
@@ -458,8 +481,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
 constexpr int kDots = 4;
 
 template <int WARPS>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) combine_grad_kernel(MoveParams p) {
     __shared__ float s_dot[kWarps][kDots];
+    wait_for_stream();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = WARPS == 1 ? 0 : warp;
     const int groups = (p.topk + kDots - 1) / kDots;
@@ -550,10 +574,6 @@ int sm_count() {
     return cached[dev];
 }
 
-cudaError_t zero_word(float* amax, cudaStream_t s) {
-    return amax ? cudaMemsetAsync(amax, 0, sizeof(float), s) : cudaSuccess;
-}
-
 MoveParams move_params(const MoveArgs& a) {
     MoveParams p{};
     p.src = static_cast<const __nv_bfloat16*>(a.src);
@@ -576,9 +596,26 @@ MoveParams move_params(const MoveArgs& a) {
 
 // Enough CTAs for the units, at most 8 (2048 threads) on each SM.
 int grid_for_units(int64_t units) { return (int)std::max<int64_t>(1, std::min<int64_t>(units, (int64_t)sm_count() * 8)); }
-int64_t zero_units_host(const MoveArgs& a) { return ceil_div(a.rows, 32) * ceil_div(a.cols, 1024); }
+int64_t zero_units_host(const MoveArgs& a) { return ceil_div(a.rows, kZeroRows) * ceil_div(a.cols, 1024); }
+
+__global__ void zero_word_kernel(float* word) {
+    wait_for_stream();
+    if (threadIdx.x == 0) *word = 0.0f;
+}
 
 }  // namespace
+
+// A maximum starts at 0.  (A memset in front of a kernel costs 3 us in a chain of small kernels, this 1.5.)
+cudaError_t zero_word(float* amax, cudaStream_t s) {
+    return amax ? launch_early(zero_word_kernel, 1, 32, 0, s, 1, amax) : cudaSuccess;
+}
+
+// Room for the sums of either row tile: the smaller one is only taken with fewer than 4 tiles of 128 rows x 256
+// columns to an SM.
+size_t act_grad_workspace(int64_t M, int64_t N) {
+    const bool few = ceil_div(M, kRowTile) * ceil_div(N, kColTile) < 4 * (int64_t)sm_count();
+    return (size_t)(ceil_div(M, few ? kRowTileFew : kRowTile) * N) * sizeof(float);
+}
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches) {
     ActGradParams p{};
@@ -594,28 +631,28 @@ cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches)
     p.counts = a.counts;
     p.experts = (int)a.experts;
     p.amax = a.amax;
-    const int64_t tiles = ceil_div(a.M, kRowTile);
+    p.strips = ceil_div(a.N, kColTile);
+    p.tile_rows = (int)(ceil_div(a.M, kRowTile) * p.strips < 4 * (int64_t)sm_count() ? kRowTileFew : kRowTile);
+    const int64_t tiles = ceil_div(a.M, p.tile_rows);
     const bool direct = a.dbias && tiles == 1 && !a.offsets;   // one row tile: its sums are the result
     p.sums = direct ? a.dbias : a.dbias ? a.workspace : nullptr;
     cudaError_t e = zero_word(a.amax, s);
     if (e != cudaSuccess) return e;
-    p.strips = ceil_div(a.N, kColTile);
     const unsigned grid = (unsigned)(tiles * p.strips);
     switch (a.act) {
-        case ACT_RELU: act_grad_kernel<ACT_RELU><<<grid, kThreads, 0, s>>>(p); break;
-        case ACT_RELU2: act_grad_kernel<ACT_RELU2><<<grid, kThreads, 0, s>>>(p); break;
-        case ACT_GELU: act_grad_kernel<ACT_GELU><<<grid, kThreads, 0, s>>>(p); break;
-        case ACT_GELU_TANH: act_grad_kernel<ACT_GELU_TANH><<<grid, kThreads, 0, s>>>(p); break;
-        case ACT_SILU: act_grad_kernel<ACT_SILU><<<grid, kThreads, 0, s>>>(p); break;
-        default: act_grad_kernel<ACT_NONE><<<grid, kThreads, 0, s>>>(p); break;
+        case ACT_RELU: e = launch_early(act_grad_kernel<ACT_RELU>, grid, kThreads, 0, s, 1, p); break;
+        case ACT_RELU2: e = launch_early(act_grad_kernel<ACT_RELU2>, grid, kThreads, 0, s, 1, p); break;
+        case ACT_GELU: e = launch_early(act_grad_kernel<ACT_GELU>, grid, kThreads, 0, s, 1, p); break;
+        case ACT_GELU_TANH: e = launch_early(act_grad_kernel<ACT_GELU_TANH>, grid, kThreads, 0, s, 1, p); break;
+        case ACT_SILU: e = launch_early(act_grad_kernel<ACT_SILU>, grid, kThreads, 0, s, 1, p); break;
+        default: e = launch_early(act_grad_kernel<ACT_NONE>, grid, kThreads, 0, s, 1, p); break;
     }
-    *launches += 1;
-    e = cudaGetLastError();
+    *launches += a.amax ? 2 : 1;
     if (e != cudaSuccess || !a.dbias || direct) return e;
     const dim3 bgrid((unsigned)ceil_div(a.N, 64), (unsigned)(a.offsets ? a.experts : 1));
-    bias_grad_kernel<<<bgrid, kThreads, 0, s>>>(a.workspace, a.M, a.N, a.offsets, a.counts, a.dbias);
     *launches += 1;
-    return cudaGetLastError();
+    return launch_early(bias_grad_kernel, bgrid, kThreads, 0, s, 1, a.workspace, a.M, a.N, p.tile_rows, a.offsets, a.counts,
+                        a.dbias);
 }
 
 // CTAs of the sort: about 1024 copies each, fewer where the table of counts
@@ -640,40 +677,38 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t s, int* launches) {
     const int ctas = (int)ceil_div(a.n, p.chunk);
     const int smem = (int)(((kWarps + 2) * a.experts + 1) * 4);   // at most 41 KB: 1024 experts
     if (ctas > 1) {
-        sort_count_kernel<<<ctas, kThreads, p.experts * 4, s>>>(p);
         *launches += 1;
+        cudaError_t e = launch_early(sort_count_kernel, ctas, kThreads, p.experts * 4, s, 1, p);
+        if (e != cudaSuccess) return e;
     }
-    sort_place_kernel<<<ctas, kThreads, smem, s>>>(p);
     *launches += 1;
-    return cudaGetLastError();
+    return launch_early(sort_place_kernel, ctas, kThreads, smem, s, 1, p);
 }
 
 cudaError_t launch_moe_gather(const MoveArgs& a, cudaStream_t s, int* launches) {
     cudaError_t e = zero_word(a.amax, s);
     if (e != cudaSuccess) return e;
     const int64_t units = a.tokens * ceil_div(a.cols, 1024) + zero_units_host(a);
-    gather_kernel<<<grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s>>>(move_params(a));
-    *launches += 1;
-    return cudaGetLastError();
+    *launches += a.amax ? 2 : 1;
+    return launch_early(gather_kernel, grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s, 1, move_params(a));
 }
 
 cudaError_t launch_moe_combine(const MoveArgs& a, cudaStream_t s, int* launches) {
-    const int64_t units = a.tokens * ceil_div(a.cols, 512);
-    combine_kernel<<<grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s>>>(move_params(a));
     *launches += 1;
-    return cudaGetLastError();
+    const int64_t units = a.tokens * ceil_div(a.cols, 256 * VECS);
+    return launch_early(combine_kernel, grid_for_units(ceil_div(units, kWarps)), kThreads, 0, s, 1, move_params(a));
 }
 
 cudaError_t launch_moe_combine_grad(const MoveArgs& a, cudaStream_t s, int* launches) {
     cudaError_t e = zero_word(a.amax, s);
     if (e != cudaSuccess) return e;
     const int64_t units = a.tokens * ceil_div(a.topk, kDots), zeros = zero_units_host(a);
+    *launches += a.amax ? 2 : 1;
     if (units >= 16 * (int64_t)sm_count())
-        combine_grad_kernel<1><<<grid_for_units(ceil_div(units + zeros, kWarps)), kThreads, 0, s>>>(move_params(a));
-    else
-        combine_grad_kernel<kWarps><<<grid_for_units(units + ceil_div(zeros, kWarps)), kThreads, 0, s>>>(move_params(a));
-    *launches += 1;
-    return cudaGetLastError();
+        return launch_early(combine_grad_kernel<1>, grid_for_units(ceil_div(units + zeros, kWarps)), kThreads, 0, s, 1,
+                            move_params(a));
+    return launch_early(combine_grad_kernel<kWarps>, grid_for_units(units + ceil_div(zeros, kWarps)), kThreads, 0, s, 1,
+                        move_params(a));
 }
 
 }  // namespace nvfp4
