@@ -860,10 +860,8 @@ __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, in
     const int row0 = t.m0 + (int)rank * 128 + q * 32;
     const int col0 = t.n0 + half * 128;
     const int ncols = p.N - col0, rows = t.row_end - row0;
-    const bool dead = row0 + lane >= t.row_live;    // a row of zeros
-    const bool some_dead = row0 + 32 > t.row_live;  // the same in every lane
-    const int64_t row = (MODE == KSEG ? (int64_t)t.e * p.M : 0) + row0;   // of C
-    const __nv_bfloat16* residual = p.residual + (row + lane) * p.ldr + col0;   // not followed where there is none
+    const int live = t.row_live - row0;             // rows of the 32 that are not zeros
+    const int64_t row = MODE == KSEG ? (int64_t)t.e * p.M + row0 : row0;   // of C
     const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + ACC_COL + half * 128;
     const int expert = MODE == ROWS ? t.e : 0;
     float2 alpha = out_scales(p, expert);
@@ -925,7 +923,7 @@ __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, in
                     if (i == g) stage_ready(lane);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = pack_bf16(u[i][j].x, u[i][j].y);
-                    if (some_dead && dead) {
+                    if (lane >= live) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = 0u;
                     }
@@ -939,19 +937,18 @@ __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, in
             const int ni = n - 32 * (i - g);
             float2* v = u[i];
             if constexpr (MODE != KSEG) {
-                uint32_t res[16];
-                if (p.residual && !dead) load_row(residual + 32 * i, res, ni);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = act_value2<ACT>(v[j]);
-                if (p.residual && !dead) {
+                if (p.residual && lane < live) {   // w serves: 16 more registers would spill
+                    load_row(p.residual + (row + lane) * p.ldr + col0 + 32 * i, w, ni);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], make_float2(bf16_lo(res[j]), bf16_hi(res[j])));
+                    for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], make_float2(bf16_lo(w[j]), bf16_hi(w[j])));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __fmul2_rn(v[j], scale);
             }
-            if (some_dead && dead) {
+            if (lane >= live) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = make_float2(0.0f, 0.0f);
             }

@@ -53,14 +53,18 @@ __device__ __forceinline__ uint32_t absmax8(uint32_t acc, const uint4& w) {
 
 // Fold every thread's packed |bf16| maximum into *amax (binary32, zeroed by
 // the caller): one atomic per CTA, none where the word is already as large.
-__device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
+__device__ __forceinline__ uint32_t cta_max(uint32_t m) {   // the result in thread 0
     __shared__ uint32_t s_max[kWarps];
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, absmax2_fold(acc));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
     __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kWarps; ++w) m = max(m, s_max[w]);
+    return m;
+}
+__device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
+    const uint32_t b = cta_max(absmax2_fold(acc));
     if (threadIdx.x == 0) {
-        uint32_t b = 0;
-        for (int w = 0; w < kWarps; ++w) b = max(b, s_max[w]);
         uint32_t* word = reinterpret_cast<uint32_t*>(amax);
         if (b > *reinterpret_cast<volatile uint32_t*>(word)) atomicMax(word, b);
     }
@@ -90,7 +94,8 @@ struct ActGradParams {
     const int* counts;
     int experts;
     float* sums;           // [row tiles x N], or dbias itself when one row tile is all there is; nullable
-    float* amax;           // nullable
+    float* amax;           // nullable: one word for all CTAs
+    uint32_t* maxima;      // nullable: a word for each CTA instead
 };
 
 // Rows of the row tile at m0 that belong to tokens: all of M, or those inside
@@ -185,14 +190,29 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
         }
     }
     if (p.amax) publish_amax(p.amax, peak);
+    if (p.maxima) {
+        const uint32_t m = cta_max(absmax2_fold(peak));
+        if (threadIdx.x == 0) p.maxima[blockIdx.x] = m;
+    }
 }
 
 // dbias [experts x N] from the sums of the row tiles: 64 columns per CTA, the
-// tiles of a segment dealt to 4 threads per column, then added in order.
+// tiles of a segment dealt to 4 threads per column, then added in order.  With
+// `amax`, one more CTA takes the maximum of the first kernel's CTAs.
 __global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __restrict__ sums, int64_t M, int64_t N,
-                                                             int tile_rows, const int* offsets, const int* counts, float* dbias) {
+                                                             int tile_rows, const int* offsets, const int* counts, float* dbias,
+                                                             const uint32_t* maxima, int n_maxima, float* amax) {
     __shared__ float s[4][64];
     wait_for_stream();
+    if ((int64_t)blockIdx.x * 64 >= N) {
+        if (blockIdx.y) return;
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n_maxima; i += kThreads) m = max(m, __ldg(maxima + i));
+        m = cta_max(m);
+        if (threadIdx.x == 0) *amax = __uint_as_float(m);
+        return;
+    }
     const int e = blockIdx.y, part = threadIdx.x >> 6, c = threadIdx.x & 63;
     const int64_t col = (int64_t)blockIdx.x * 64 + c;
     const int64_t tiles = (M + tile_rows - 1) / tile_rows;
@@ -610,11 +630,12 @@ cudaError_t zero_word(float* amax, cudaStream_t s) {
     return amax ? launch_early(zero_word_kernel, 1, 32, 0, s, 1, amax) : cudaSuccess;
 }
 
-// Room for the sums of either row tile: the smaller one is only taken with fewer than 4 tiles of 128 rows x 256
-// columns to an SM.
+static int64_t act_grad_tile_rows(int64_t M, int64_t N) {
+    return ceil_div(M, kRowTile) * ceil_div(N, kColTile) < 4 * (int64_t)sm_count() ? kRowTileFew : kRowTile;
+}
+// The sums of the row tiles and the maxima of the CTAs.
 size_t act_grad_workspace(int64_t M, int64_t N) {
-    const bool few = ceil_div(M, kRowTile) * ceil_div(N, kColTile) < 4 * (int64_t)sm_count();
-    return (size_t)(ceil_div(M, few ? kRowTileFew : kRowTile) * N) * sizeof(float);
+    return (size_t)(ceil_div(M, act_grad_tile_rows(M, N)) * (N + ceil_div(N, kColTile))) * sizeof(float);
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches) {
@@ -632,12 +653,20 @@ cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches)
     p.experts = (int)a.experts;
     p.amax = a.amax;
     p.strips = ceil_div(a.N, kColTile);
-    p.tile_rows = (int)(ceil_div(a.M, kRowTile) * p.strips < 4 * (int64_t)sm_count() ? kRowTileFew : kRowTile);
+    p.tile_rows = (int)act_grad_tile_rows(a.M, a.N);
     const int64_t tiles = ceil_div(a.M, p.tile_rows);
     const bool direct = a.dbias && tiles == 1 && !a.offsets;   // one row tile: its sums are the result
     p.sums = direct ? a.dbias : a.dbias ? a.workspace : nullptr;
-    cudaError_t e = zero_word(a.amax, s);
-    if (e != cudaSuccess) return e;
+    const bool second = a.dbias && !direct;   // a second kernel, which then takes the maximum too
+    cudaError_t e = cudaSuccess;
+    if (second && a.amax) {
+        p.amax = nullptr;
+        p.maxima = reinterpret_cast<uint32_t*>(a.workspace + tiles * a.N);
+    } else if (a.amax) {
+        *launches += 1;
+        e = zero_word(a.amax, s);
+        if (e != cudaSuccess) return e;
+    }
     const unsigned grid = (unsigned)(tiles * p.strips);
     switch (a.act) {
         case ACT_RELU: e = launch_early(act_grad_kernel<ACT_RELU>, grid, kThreads, 0, s, 1, p); break;
@@ -647,12 +676,12 @@ cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s, int* launches)
         case ACT_SILU: e = launch_early(act_grad_kernel<ACT_SILU>, grid, kThreads, 0, s, 1, p); break;
         default: e = launch_early(act_grad_kernel<ACT_NONE>, grid, kThreads, 0, s, 1, p); break;
     }
-    *launches += a.amax ? 2 : 1;
-    if (e != cudaSuccess || !a.dbias || direct) return e;
-    const dim3 bgrid((unsigned)ceil_div(a.N, 64), (unsigned)(a.offsets ? a.experts : 1));
+    *launches += 1;
+    if (e != cudaSuccess || !second) return e;
+    const dim3 bgrid((unsigned)(ceil_div(a.N, 64) + (a.amax ? 1 : 0)), (unsigned)(a.offsets ? a.experts : 1));
     *launches += 1;
     return launch_early(bias_grad_kernel, bgrid, kThreads, 0, s, 1, a.workspace, a.M, a.N, p.tile_rows, a.offsets, a.counts,
-                        a.dbias);
+                        a.dbias, p.maxima, (int)grid, a.amax);
 }
 
 // CTAs of the sort: about 1024 copies each, fewer where the table of counts

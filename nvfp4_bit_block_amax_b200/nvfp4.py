@@ -513,7 +513,7 @@ def _padded(rows: int, cols: int, dtype, device) -> torch.Tensor:
     """A [rows x cols] view whose row stride is a multiple of 8 elements."""
     ld = (cols + 7) // 8 * 8
     t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    return t if ld == cols else t.narrow(1, 0, cols)
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -625,13 +625,13 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
     assert expert_ids.dtype is torch.int32 and expert_ids.dim() == 2 and expert_ids.is_contiguous()
     n = expert_ids.numel()
     if rows is None:
-        rows = nvfp4_moe_rows(n, experts)
+        rows = (n + 127 * min(n, experts) + 127) // 128 * 128        # nvfp4_moe_rows
     ws_bytes = nvfp4_moe_workspace_size(n, experts)
     # one allocation: the call's scratch, then the plan's four arrays
     buf = _kept(torch.empty(ws_bytes // 4 + 2 * experts + 1 + rows + n, dtype=torch.int32, device=expert_ids.device), stream)
     ws, offsets, counts, row_copy, copy_row = buf.split((ws_bytes // 4, experts + 1, experts, rows, n))
     nvfp4_moe_sort(expert_ids, n, experts, rows, offsets, counts, row_copy, copy_row, ws, ws_bytes, stream)
-    return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))
+    return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))   # checks its shapes
 
 
 def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = None,
