@@ -46,16 +46,21 @@ constexpr uint32_t F_TMEM = 256;
 // TOK: most tokens of one pass.
 template <int TOK>
 struct Layout {
-    static constexpr int kStages = TOK == 32 ? 4 : 3;
+    static constexpr int kStages = TOK == 128 ? 3 : 4;
     static constexpr int kX = TOK * F_BKB;
     static constexpr int kStage = F_W_STAGE + kX + 2 * F_SF_STAGE;
     static constexpr int kOffX = F_W_STAGE, kOffSfw = kOffX + kX, kOffSfx = kOffSfw + F_SF_STAGE;
-    static constexpr int kOffBar = kStages * kStage;   // full, empty, scales per stage; accumulator, drain
+    // Partial sums of a cluster, [CTA][token][feature]: with few tokens in memory of their own, else in the stages,
+    // which the cluster first has to be done with.
+    static constexpr bool kOwnSums = TOK == 16;
+    static constexpr int kOffSums = kOwnSums ? kStages * kStage : 0;
+    static constexpr int kOffBar = kStages * kStage + (kOwnSums ? TOK * F_ROWS * 4 : 0);
     static constexpr int kOffMisc = kOffBar + (3 * kStages + 2) * 8;
     static constexpr int kBytes = kOffMisc + 16 + 1008;
     static constexpr uint32_t kSf = TOK;               // first tensor-memory column of the scales, 32 per stage
     static_assert(kStage % 1024 == 0 && kSf + kStages * 32 <= F_TMEM, "layout");
-    static_assert(TOK >= 8 && TOK * F_ROWS * 4 <= kOffBar, "partial sums of a cluster fit in the stages");
+    static_assert(TOK >= 8 && kOffSums + TOK * F_ROWS * 4 <= kOffBar, "partial sums of a cluster of up to 8");
+    // full, empty, scales per stage; accumulator, drain: at kOffBar
 };
 
 struct FewParams {
@@ -205,6 +210,8 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const int kb0 = (int)((int64_t)blocks * rank / splits), kb1 = (int)((int64_t)blocks * (rank + 1) / splits);
 
     if (threadIdx.x == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_x);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
@@ -228,6 +235,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (L::kOwnSums && splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA runs
     const uint32_t tmem = *tmem_slot;
 
     Finish f;
@@ -245,7 +253,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     int s = 0;                      // stage and its phase, of each role
     uint32_t phase = 0, acc_phase = 0;
     uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
-    bool ok = true;
+    bool ok = true, freed = false;
     for (int t0 = start; t0 < stop; t0 += TOK) {      // a pass over the weight for up to TOK tokens
         const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
         if (warp == 0) {
@@ -307,14 +315,18 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         }
         acc_phase ^= 1;
         __syncwarp();
-        // The stages' memory takes the partial sums, [CTA][token][feature], of the tokens that a CTA finishes: all
-        // of them, or in a cluster a share.  Every MMA that reads a stage has to be done for that, in all its CTAs.
+        // Shared memory takes the partial sums, [CTA][token][feature], of the tokens that a CTA finishes: all of them, or in
+        // a cluster a share.
         int shift = 0;              // a share is 2^shift tokens
         while ((splits << shift) < tokens) ++shift;
-        if (splits > 1) cluster_sync();
+        if (splits > 1) {
+            // Every CTA of the cluster runs, and its stages (or, with sums of their own, those of the pass before) are free.
+            if (L::kOwnSums && t0 == start) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            else cluster_sync();
+        }
         if (warp >= 2) {
             const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t col = sbase + 4 * ((warp & 3) * 32 + lane) + (rank << shift) * F_ROWS * 4;
+            const uint32_t col = sbase + L::kOffSums + 4 * ((warp & 3) * 32 + lane) + (rank << shift) * F_ROWS * 4;
             for (int b = 0; b < boxes; ++b) {
                 uint32_t v[16];
                 tc_ld_32x32b_x16(tlane + 16 * b, v);
@@ -329,10 +341,16 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 }
             }
         }
+        tc_fence_before();
         if (splits > 1) cluster_sync();
         else __syncthreads();
+        if (warp == 1 && t0 + TOK >= stop && !*abort_flag) {   // the last pass: nothing needs tensor memory any more
+            freed = true;
+            tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
+        }
         {
-            const float4* part = reinterpret_cast<const float4*>(smem) + lane;
+            const float4* part = reinterpret_cast<const float4*>(smem + L::kOffSums) + lane;
             const int first = rank << shift, count = min(1 << shift, tokens - first);
             for (int t = warp; t < count; t += F_THREADS / 32) {
                 float4 sum = part[t * (F_ROWS / 4)];
@@ -390,7 +408,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (p.c_amax && threadIdx.x == 0 && *s_amax) atomicMax(p.c_amax, *s_amax);
-    if (warp == 1) {
+    if (warp == 1 && !freed) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
     }
@@ -421,6 +439,7 @@ int prepared_sms() {
         int n = 0;
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         for (int act = 0; act < kNumActivations; ++act) {
+            cudaFuncSetAttribute(few_kernel<16>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<16>::kBytes);
             cudaFuncSetAttribute(few_kernel<32>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<32>::kBytes);
             cudaFuncSetAttribute(few_kernel<128>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kBytes);
         }
@@ -463,9 +482,10 @@ cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
     const int64_t units = (int64_t)p.tiles * p.experts, blocks = ceil_div(g.K, 256);
     int splits = 1;
     while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
-    const bool small = !g.offsets && g.M <= 32;
-    return launch_early(small ? few_kernel<32>(g.act) : few_kernel<128>(g.act), (unsigned)(units * splits), F_THREADS,
-                        small ? Layout<32>::kBytes : Layout<128>::kBytes, s, splits, mw, mx, p);
+    const int tokens = g.offsets ? 128 : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
+    FewKernel kernel = tokens == 16 ? few_kernel<16>(g.act) : tokens == 32 ? few_kernel<32>(g.act) : few_kernel<128>(g.act);
+    const int smem = tokens == 16 ? Layout<16>::kBytes : tokens == 32 ? Layout<32>::kBytes : Layout<128>::kBytes;
+    return launch_early(kernel, (unsigned)(units * splits), F_THREADS, smem, s, splits, mw, mx, p);
 }
 
 unsigned int* few_error_word() {
