@@ -370,6 +370,16 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
                      nullptr, stream, 1);
 }
 
+// Whether the product for few rows is the faster one (us, it against the large product, on one B200):
+//   M x 14336 x 4096     64: 13.8 / 15.8   96: 16.1 / 16.0   128: 17.2 / 16.1   192: 27 / 16
+//   M x 28672 x 8192     64: 31.0 / 38.3                     128: 36.8 / 39.3   192: 65 / 40
+//   M x 4096 x 14336     64: 14.0 / 31.1                     128: 18.4 / 31.4   192: 28 / 31
+//   M x 1024 x 1024      64:  7.5 /  9.4   96:  9.9 /  9.5   128: 10.9 /  9.7   192: 17 / 10
+// so up to 128 rows.  How many rows each expert has is not known here, but segments are padded to 128: with
+// nvfp4_moe_rows, M / experts is about 127 more than the mean.  Mean 2 and 8 rows, 8 experts of 14336 x 4096: 58 / 66 and
+// 69 / 73, 64 of 2048 x 2048: 44 / 65 and 54 / 57; mean 32: 83 / 73 and 65 / 58.  So up to a mean of 16.
+static bool few_rows(const GemmExtArgs& g) { return g.experts ? g.M <= (127 + 16) * g.experts + 127 : g.M <= 128; }
+
 static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
     if (!g.a || !g.sfa || !g.a_gs || !g.b || !g.sfb || !g.b_gs || !g.c) return NVFP4_ERR_INVALID_ARG;
     if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_INVALID_ARG;
@@ -389,7 +399,7 @@ static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
         return NVFP4_ERR_MISALIGNED;
     g.out_bf16 = out_dtype == NVFP4_OUT_BF16;
     if (zero_word(g.c_amax, static_cast<cudaStream_t>(stream)) != cudaSuccess) return NVFP4_ERR_CUDA;
-    const bool few = !g.wgrad && (g.experts ? g.M <= 128 * (g.experts + 1) : g.M <= 128);
+    const bool few = !g.wgrad && few_rows(g);
     cudaError_t e = (few ? launch_gemm_few : launch_gemm_ext)(g, static_cast<cudaStream_t>(stream));
     g_launches += g.c_amax ? 2 : 1;
     return from_cuda(e);

@@ -1,5 +1,5 @@
 // few.cu -- the linear layer's product for few rows (tokens): one to 128, and
-// experts that have about as many rows each.
+// experts that have a few rows each.
 //
 // C[t][n] = act(alpha sum_k x_tk w_nk + bias_n) + residual_tn.  With few rows
 // the weight is read once and hardly used: 0.5625 bytes per element against
@@ -292,6 +292,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             }
         } else {
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const int quarter = (t0 >> 5) & 3;
             for (int kb = kb0; kb < kb1 && ok; ++kb) {
                 if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
                 const uint32_t sf = sbase + s * L::kStage + L::kOffSfw + 16 * lane;
@@ -300,7 +301,9 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 for (int j = 0; j < 4; ++j) {
                     const uint4 a = lds128(sf + 512 * j), b = lds128(sf + F_SF_STAGE + 512 * j);
                     w[4 * j] = a.x; w[4 * j + 1] = a.y; w[4 * j + 2] = a.z; w[4 * j + 3] = a.w;
-                    x[4 * j] = b.x; x[4 * j + 1] = b.y; x[4 * j + 2] = b.z; x[4 * j + 3] = b.w;
+                    // 32 rows to a column: a pass of up to 32 tokens starts at the column of its rows in the chunk of 128
+                    x[4 * j] = TOK == 128 || quarter == 0 ? b.x : quarter == 1 ? b.y : quarter == 2 ? b.z : b.w;
+                    x[4 * j + 1] = b.y; x[4 * j + 2] = b.z; x[4 * j + 3] = b.w;
                 }
                 tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32, w);
                 tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32 + 16, x);
@@ -482,7 +485,7 @@ cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
     const int64_t units = (int64_t)p.tiles * p.experts, blocks = ceil_div(g.K, 256);
     int splits = 1;
     while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
-    const int tokens = g.offsets ? 128 : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
+    const int tokens = g.offsets ? 32 : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
     FewKernel kernel = tokens == 16 ? few_kernel<16>(g.act) : tokens == 32 ? few_kernel<32>(g.act) : few_kernel<128>(g.act);
     const int smem = tokens == 16 ? Layout<16>::kBytes : tokens == 32 ? Layout<32>::kBytes : Layout<128>::kBytes;
     return launch_early(kernel, (unsigned)(units * splits), F_THREADS, smem, s, splits, mw, mx, p);

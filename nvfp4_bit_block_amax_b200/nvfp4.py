@@ -133,11 +133,7 @@ def lib():
 
 def _p(t) -> Optional[int]:
     """Device pointer of a tensor (None / int pass through)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
@@ -509,10 +505,10 @@ def _matrix(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> int:
     return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _padded(rows: int, cols: int, dtype, device) -> torch.Tensor:
-    """A [rows x cols] view whose row stride is a multiple of 8 elements."""
+def _padded(rows: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    """A [rows x cols] view, on the device of `like`, whose row stride is a multiple of 8 elements."""
     ld = (cols + 7) // 8 * 8
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
+    t = like.new_empty((rows, ld), dtype=dtype)
     return t if ld == cols else t.narrow(1, 0, cols)
 
 
@@ -563,7 +559,7 @@ def _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, 
     _check_word(amax_out)
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
     if out is None:
-        out = _padded(M, N, dt, a_codes.device)
+        out = _padded(M, N, dt, a_codes)
     ldc = _matrix(out, M, N, dt)
     ldr = _matrix(residual, M, N) if residual is not None else 0
     ldp = _matrix(pre, M, N) if pre is not None else 0
@@ -586,14 +582,14 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_
     ldy = _matrix(dy, M, N)
     ldz = _matrix(z, M, N) if z is not None else 0
     if out is None:
-        out = _padded(M, N, torch.bfloat16, dy.device)
+        out = _padded(M, N, torch.bfloat16, dy)
     lddz = _matrix(out, M, N)
     _check_word(amax_out)
     dbias = ws = None
     experts = 0 if plan is None else plan.experts
     assert plan is None or plan.rows == M
     if bias_grad:
-        dbias = torch.empty((experts, N) if experts else (N,), dtype=torch.float32, device=dy.device)
+        dbias = dy.new_empty((experts, N) if experts else (N,), dtype=torch.float32)
         ws = _scratch(nvfp4_act_grad_workspace_size(M, N), dy.device, stream)
     nvfp4_act_grad(dy, ldy, z, ldz, M, N, activation, plan.offsets if experts else None,
                    plan.counts if experts else None, experts, out, lddz, dbias, amax_out, ws,
@@ -628,7 +624,7 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
         rows = (n + 127 * min(n, experts) + 127) // 128 * 128        # nvfp4_moe_rows
     ws_bytes = nvfp4_moe_workspace_size(n, experts)
     # one allocation: the call's scratch, then the plan's four arrays
-    buf = _kept(torch.empty(ws_bytes // 4 + 2 * experts + 1 + rows + n, dtype=torch.int32, device=expert_ids.device), stream)
+    buf = _kept(expert_ids.new_empty(ws_bytes // 4 + 2 * experts + 1 + rows + n), stream)
     ws, offsets, counts, row_copy, copy_row = buf.split((ws_bytes // 4, experts + 1, experts, rows, n))
     nvfp4_moe_sort(expert_ids, n, experts, rows, offsets, counts, row_copy, copy_row, ws, ws_bytes, stream)
     return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))   # checks its shapes
@@ -640,7 +636,7 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = Non
     `amax_out` (a device float) also max |x|, for the quantizers.  Its gradient is moe_combine without weights."""
     cols = x.shape[1]
     if out is None:
-        out = torch.empty(plan.rows, cols, dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((plan.rows, cols))
     _check_word(amax_out)
     nvfp4_moe_gather(x, _matrix(x, plan.tokens, cols), plan.tokens, plan.topk, cols, plan.copy_row, plan.row_copy,
                      plan.rows, out, _matrix(out, plan.rows, cols), amax_out, stream)
@@ -659,7 +655,7 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] 
     cols = y.shape[1]
     _check_weights(weights, plan)
     if out is None:
-        out = torch.empty(plan.tokens, cols, dtype=torch.bfloat16, device=y.device)
+        out = y.new_empty((plan.tokens, cols))
     nvfp4_moe_combine(y, _matrix(y, plan.rows, cols), plan.rows, cols, plan.copy_row, weights, residual,
                       _matrix(residual, plan.tokens, cols) if residual is not None else 0, plan.tokens, plan.topk,
                       out, _matrix(out, plan.tokens, cols), stream)
@@ -673,8 +669,8 @@ def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], plan: MoePla
     cols = dout.shape[1]
     _check_weights(weights, plan)
     _check_word(amax_out)
-    dy = torch.empty(plan.rows, cols, dtype=torch.bfloat16, device=dout.device)
-    dw = torch.empty(plan.copy_row.shape, dtype=torch.float32, device=dout.device) if y is not None else None
+    dy = dout.new_empty((plan.rows, cols))
+    dw = dout.new_empty(plan.copy_row.shape, dtype=torch.float32) if y is not None else None
     nvfp4_moe_combine_grad(dout, _matrix(dout, plan.tokens, cols), y,
                            _matrix(y, plan.rows, cols) if y is not None else 0, plan.tokens, plan.topk, cols,
                            plan.copy_row, plan.row_copy, plan.rows, weights, dy, cols, dw, amax_out, stream)
@@ -705,7 +701,7 @@ def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs,
     _check_operand(b_codes, b_scales_mma, b_gs, N, K)
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
     if out is None:
-        out = _padded(plan.experts * M, N, dt, a_codes.device).unflatten(0, (plan.experts, M))
+        out = _padded(plan.experts * M, N, dt, a_codes).unflatten(0, (plan.experts, M))
     assert out.dtype == dt and out.shape == (plan.experts, M, N) and out.stride(2) == 1
     assert plan.experts == 1 or out.stride(0) == M * out.stride(1)
     nvfp4_gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan.offsets, plan.counts,
