@@ -388,7 +388,7 @@ static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
         return NVFP4_ERR_INVALID_ARG;
     if ((g.residual && g.ldr < g.N) || (g.pre && g.ldp < g.N)) return NVFP4_ERR_INVALID_ARG;
     if (g.experts && (!g.offsets || !g.counts || g.experts < 1 || g.experts > kMaxExpertsArg ||
-                      g.experts * g.N >= kMaxDim || g.experts * g.M >= kMaxDim * 128))
+                      g.experts * g.N >= kMaxDim || (g.wgrad && g.experts * g.M >= kMaxDim)))
         return NVFP4_ERR_INVALID_ARG;
     if (g.experts && !g.wgrad && g.M > kMaxSortedRows) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (g.K % 64 || (g.experts && (g.wgrad ? g.K : g.M) % 128)) return NVFP4_ERR_UNSUPPORTED_SHAPE;

@@ -497,9 +497,15 @@ def quantize_dual(x: torch.Tensor, rounding: int = NVFP4_RNE, sr_seed: int = 0, 
 
 
 # ------------------------------------------------------ the linear layer ----
+def _here(t: torch.Tensor):
+    """Launches go to the current device: a tensor elsewhere (host memory included) is refused."""
+    assert t.get_device() == torch._C._cuda_getDevice(), f"tensor on {t.device}, not on the current CUDA device"
+
+
 def _matrix(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> int:
     """Row stride of a [rows x cols] matrix with unit column stride (checked)."""
     assert t.dtype is dtype and t.shape == (rows, cols)
+    _here(t)
     ld, unit = t.stride()
     assert unit == 1 or cols == 1
     return ld if rows > 1 else (cols + 7) // 8 * 8
@@ -530,10 +536,14 @@ def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
     need = (rows + 127) // 128 * ((k // 16 + 3) // 4) * 512      # nvfp4_mma_scale_bytes
     assert scales_mma.numel() >= experts * need and scales_mma.is_contiguous()
     assert gs.dtype is torch.float32 and gs.numel() == experts and gs.is_contiguous()
+    for t in (codes, scales_mma, gs):
+        _here(t)
 
 
 def _check_word(t):
-    assert t is None or (t.dtype is torch.float32 and t.numel() == 1)
+    if t is not None:
+        assert t.dtype is torch.float32 and t.numel() == 1
+        _here(t)
 
 
 def gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: int, K: int, bias=None,
@@ -555,7 +565,8 @@ def _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, 
                 out_dtype, out, pre, amax_out, stream):
     experts = 1 if plan is None else plan.experts
     if bias is not None:
-        assert bias.dtype == torch.bfloat16 and bias.is_contiguous() and bias.numel() == experts * N
+        assert bias.dtype is torch.bfloat16 and bias.is_contiguous() and bias.numel() == experts * N
+        _here(bias)
     _check_word(amax_out)
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
     if out is None:
@@ -579,6 +590,7 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_
     """(dz, dbias) of C = act(z) + residual with z = product + bias: dz = dy * act'(z) in bf16, dbias its column
     sums in fp32 ([N], with a plan [experts x N]; None without bias_grad).  z is the `pre` of gemm_epilogue."""
     M, N = dy.shape
+    assert plan is None or plan.rows == M
     ldy = _matrix(dy, M, N)
     ldz = _matrix(z, M, N) if z is not None else 0
     if out is None:
@@ -587,7 +599,6 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_
     _check_word(amax_out)
     dbias = ws = None
     experts = 0 if plan is None else plan.experts
-    assert plan is None or plan.rows == M
     if bias_grad:
         dbias = dy.new_empty((experts, N) if experts else (N,), dtype=torch.float32)
         ws = _scratch(nvfp4_act_grad_workspace_size(M, N), dy.device, stream)
@@ -608,7 +619,7 @@ class MoePlan:
 
     def __post_init__(self):
         for t in (self.offsets, self.counts, self.row_copy, self.copy_row):
-            assert t.dtype is torch.int32 and t.is_contiguous()
+            assert t.dtype is torch.int32 and t.is_contiguous() and t.device == self.copy_row.device
         self.experts = self.counts.numel()
         self.rows = self.row_copy.numel()
         assert self.offsets.numel() == self.experts + 1
@@ -619,6 +630,7 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
     """Sort the copies of int32 expert_ids [tokens x topk] by expert.  rows (default: enough for every routing)
     bounds the sorted matrices; copies that find no row are dropped."""
     assert expert_ids.dtype is torch.int32 and expert_ids.dim() == 2 and expert_ids.is_contiguous()
+    _here(expert_ids)
     n = expert_ids.numel()
     if rows is None:
         rows = (n + 127 * min(n, experts) + 127) // 128 * 128        # nvfp4_moe_rows
@@ -635,6 +647,7 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = Non
     """The token rows x bf16 [tokens x cols] sorted by expert: bf16 [rows x cols], zeros in padding rows.  With
     `amax_out` (a device float) also max |x|, for the quantizers.  Its gradient is moe_combine without weights."""
     cols = x.shape[1]
+    _here(plan.copy_row)
     if out is None:
         out = x.new_empty((plan.rows, cols))
     _check_word(amax_out)
@@ -644,8 +657,9 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = Non
 
 
 def _check_weights(weights, plan):
-    assert weights is None or (weights.dtype == torch.float32 and weights.is_contiguous()
-                               and weights.shape == plan.copy_row.shape)
+    if weights is not None:
+        assert weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == plan.copy_row.shape
+        _here(weights)
 
 
 def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] = None,
@@ -653,6 +667,7 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] 
                 stream=None) -> torch.Tensor:
     """residual[t] + sum_j weights[t, j] * y[row of copy (t, j)]: bf16 [tokens x cols]; weights fp32 or None (1)."""
     cols = y.shape[1]
+    _here(plan.copy_row)
     _check_weights(weights, plan)
     if out is None:
         out = y.new_empty((plan.tokens, cols))
@@ -667,6 +682,7 @@ def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], plan: MoePla
     """(dy, dweights) of moe_combine: dy bf16 [rows x cols] with zeros in padding rows, dweights fp32
     [tokens x topk] (None when y is None)."""
     cols = dout.shape[1]
+    _here(plan.copy_row)
     _check_weights(weights, plan)
     _check_word(amax_out)
     dy = dout.new_empty((plan.rows, cols))
@@ -685,6 +701,7 @@ def gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan:
     """gemm_epilogue over M rows sorted by expert: b_codes [experts x N x K/2], their scales and b_gs [experts],
     bias [experts x N].  Padding rows of C (and pre) are zeros."""
     assert plan.rows == M
+    _here(plan.counts)
     _check_operand(a_codes, a_scales_mma, a_gs, M, K)
     _check_operand(b_codes, b_scales_mma, b_gs, N, K, plan.experts)
     return _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M, N, K, bias, activation,
@@ -697,12 +714,14 @@ def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs,
     """[experts x M x N]: per expert A . B^T over its K sorted rows, A [M x K] and B [N x K] the transposed
     operands."""
     assert plan.rows == K
+    _here(plan.counts)
     _check_operand(a_codes, a_scales_mma, a_gs, M, K)
     _check_operand(b_codes, b_scales_mma, b_gs, N, K)
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
     if out is None:
         out = _padded(plan.experts * M, N, dt, a_codes).unflatten(0, (plan.experts, M))
-    assert out.dtype == dt and out.shape == (plan.experts, M, N) and out.stride(2) == 1
+    assert out.dtype is dt and out.shape == (plan.experts, M, N) and out.stride(2) == 1
+    _here(out)
     assert plan.experts == 1 or out.stride(0) == M * out.stride(1)
     nvfp4_gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan.offsets, plan.counts,
                              plan.experts, M, N, K, out_dtype, out, out.stride(1), stream)
@@ -712,7 +731,8 @@ def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs,
 def quantize_2d_experts(w: torch.Tensor, columnwise: bool = True, stream=None):
     """(W, W^T) operands of gemm_grouped from expert weights bf16 [experts x rows x cols], each quantized by
     quantize_2d: Quantized with stacked codes, scales and global scales (the second None without columnwise)."""
-    assert w.dtype == torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1
+    assert w.dtype is torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1
+    _here(w)
     experts, rows, cols = w.shape
     dev = w.device
     row = Quantized(torch.empty(experts, rows, cols // 2, dtype=torch.uint8, device=dev), None,

@@ -479,6 +479,50 @@ def test_grouped_wgrad(tokens, topk, experts, M, Nn, dtype):
             assert (got[e] == 0).all()
 
 
+@pytest.mark.parametrize("rows", [None, 4096])     # the kernel for few rows, and the large one
+def test_products_with_nothing_routed(rows):
+    """Every copy dropped: C, pre, the weight gradients and the bias gradients are zeros, whatever was there."""
+    E, Nn, K = 4, 264, 128
+    plan = N.moe_sort(torch.full((9, 2), E, dtype=torch.int32, device="cuda"), E, rows=rows)
+    R = plan.rows
+    a, b = N.quantize_1d(bf16(R, K, seed=1)), N.quantize_1d(bf16(E * Nn, K, seed=2))
+    b_scales = torch.stack([N.quantize_1d(bf16(Nn, K, seed=3)).scales_mma] * E)
+    out, pre = (torch.full((R, Nn), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    amax = torch.full((1,), -1.0, device="cuda")
+    N.gemm_grouped(*quant_args(a), b.codes, b_scales, torch.ones(E, device="cuda"), plan, R, Nn, K,
+                   bias=bf16(E, Nn, seed=4), activation=N.NVFP4_ACT_SILU, out=out, pre=pre, amax_out=amax)
+    t = N.quantize_1d(bf16(R, 64, seed=5), transpose=True)
+    dw = N.gemm_grouped_wgrad(*quant_args(t), *quant_args(t), plan, 64, 64, R,
+                              out=torch.full((E, 64, 64), 7.0, device="cuda"))
+    dz, db = N.act_grad(bf16(R, Nn, seed=6), bf16(R, Nn, seed=7), N.NVFP4_ACT_GELU, plan=plan)
+    ok()
+    assert all((x == 0).all() for x in (out, pre, dw, dz, db)) and amax.item() == 0
+
+
+@pytest.mark.parametrize("experts,count", [(1, 40), (2, 100), (3, 129), (16, 33)])
+def test_grouped_kernels_agree_where_the_choice_changes(experts, count):
+    """The same rows with a row capacity just below and above the one that decides between the two kernels."""
+    Nn, K = 264, 320
+    ids = torch.arange(experts * count, device="cuda", dtype=torch.int32)[:, None] % experts
+    x = bf16(experts * count, K, seed=41)
+    q = [N.quantize_1d(bf16(Nn, K, seed=42 + e)) for e in range(experts)]
+    b = (torch.stack([w.codes for w in q]), torch.stack([w.scales_mma for w in q]), torch.cat([w.global_scale for w in q]))
+    got = []
+    need = experts * ((count + 127) // 128 * 128)
+    for rows in (need, 143 * experts + 255 + need):
+        plan = N.moe_sort(ids.contiguous(), experts, rows=rows // 128 * 128)
+        a = N.quantize_1d(N.moe_gather(x, plan))
+        c = N.gemm_grouped(*quant_args(a), *b, plan, plan.rows, Nn, K, bias=bf16(experts, Nn, seed=43),
+                           activation=N.NVFP4_ACT_GELU_TANH, out_dtype=N.NVFP4_OUT_F32)
+        ok()
+        got.append(c[:need].to(F64))
+        av = values64(a.codes, a.scales, a.global_scale)[:need]
+        S = torch.cat([av[e * need // experts:(e + 1) * need // experts].abs()
+                       @ values64(w.codes, w.scales, w.global_scale).abs().t() for e, w in enumerate(q)])
+    # two kernels, each within the product's bound of the exact sums and two evaluations of the activation
+    assert ((got[0] - got[1]).abs() <= 2 * (1.13 * z_bound(K, S) + 2.0 ** -18 * (S + 1))).all()
+
+
 def test_act_grad_by_expert():
     plan = N.moe_sort(routing(500, 3, 9, seed=3, skew=3.0), 9)
     R, Nn = plan.rows, 260

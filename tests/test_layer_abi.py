@@ -77,6 +77,7 @@ def test_gemm_grouped_wgrad(L):
     assert refused(E=0) == ARG and refused(E=513) == ARG and refused(off=None) == ARG and refused(cnt=None) == ARG
     assert refused(ldc=120) == ARG and refused(ldc=132) == ALIGN and refused(c=FAKE + 4) == ALIGN
     assert refused(dt=5) == ARG and refused(M=0) == ARG and refused(N=0) == ARG
+    assert refused(E=512, M=1 << 22) == ARG                              # rows of C past 31 bits
 
 
 def test_act_grad(L):
@@ -147,9 +148,10 @@ def test_row_movements(L):
             assert refused(**{ld: 56}) == ARG and refused(**{ld: 68}) == ALIGN
 
 
-def test_helpers_refuse_mismatched_tensors():
+def test_helpers_refuse_mismatched_tensors(monkeypatch):
     """The torch helpers check shapes and types before they hand out pointers (CPU tensors stand in)."""
     u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    monkeypatch.setattr(N, "_here", lambda t: None)      # the device check has a test of its own
     f = torch.zeros(1)
     plan = N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 2, 256, (8, 2))))
     assert (plan.experts, plan.rows, plan.tokens, plan.topk) == (2, 256, 8, 2)
@@ -174,3 +176,25 @@ def test_helpers_refuse_mismatched_tensors():
         N.act_grad(torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(8, 63, dtype=torch.bfloat16), N.NVFP4_ACT_SILU)
     with pytest.raises(AssertionError):
         N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 3, 256, (8, 2))))
+
+
+def test_helpers_refuse_tensors_that_are_not_on_the_current_device(monkeypatch):
+    """Host tensors stand for those of another device: either would hand the kernels addresses they cannot read."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    plan = N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 2, 256, (8, 2))))
+    op = (u8(128, 32), u8(512), torch.zeros(1))
+    for call_ in (lambda: N.gemm_epilogue(*op, *op, 128, 128, 64),
+                  lambda: N.act_grad(bf(8, 64), bf(8, 64), N.NVFP4_ACT_SILU),
+                  lambda: N.moe_sort(torch.zeros(8, 2, dtype=torch.int32), 4),
+                  lambda: N.moe_gather(bf(8, 64), plan),
+                  lambda: N.moe_combine(bf(256, 64), plan),
+                  lambda: N.moe_combine_grad(bf(8, 64), bf(256, 64), plan),
+                  lambda: N.gemm_grouped(u8(256, 32), u8(1024), torch.zeros(1), u8(2, 128, 32), u8(2, 512),
+                                         torch.zeros(2), plan, 256, 128, 64),
+                  lambda: N.gemm_grouped_wgrad(u8(64, 128), u8(2048), torch.zeros(1), u8(64, 128), u8(2048),
+                                               torch.zeros(1), plan, 64, 64, 256),
+                  lambda: N.quantize_2d_experts(bf(2, 64, 64))):
+        with pytest.raises(AssertionError, match="current CUDA device"):
+            call_()
