@@ -636,10 +636,15 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
         rows = (n + 127 * min(n, experts) + 127) // 128 * 128        # nvfp4_moe_rows
     ws_bytes = nvfp4_moe_workspace_size(n, experts)
     # one allocation: the call's scratch, then the plan's four arrays
-    buf = _kept(expert_ids.new_empty(ws_bytes // 4 + 2 * experts + 1 + rows + n), stream)
-    ws, offsets, counts, row_copy, copy_row = buf.split((ws_bytes // 4, experts + 1, experts, rows, n))
-    nvfp4_moe_sort(expert_ids, n, experts, rows, offsets, counts, row_copy, copy_row, ws, ws_bytes, stream)
-    return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))   # checks its shapes
+    sizes = (ws_bytes // 4, experts + 1, experts, rows, n)
+    buf = _kept(expert_ids.new_empty(sum(sizes)), stream)
+    ws = buf.data_ptr()
+    offsets = ws + ws_bytes
+    counts = offsets + 4 * experts + 4
+    row_copy = counts + 4 * experts
+    nvfp4_moe_sort(expert_ids, n, experts, rows, offsets, counts, row_copy, row_copy + 4 * rows, ws, ws_bytes, stream)
+    _, offsets, counts, row_copy, copy_row = torch.split_with_sizes(buf, sizes)
+    return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))
 
 
 def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = None,
