@@ -376,9 +376,13 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
 //   M x 4096 x 14336     64: 14.0 / 31.1                     128: 18.4 / 31.4   192: 28 / 31
 //   M x 1024 x 1024      64:  7.5 /  9.4   96:  9.9 /  9.5   128: 10.9 /  9.7   192: 17 / 10
 // so up to 128 rows.  How many rows each expert has is not known here, but segments are padded to 128: with
-// nvfp4_moe_rows, M / experts is about 127 more than the mean.  Mean 2 and 8 rows, 8 experts of 14336 x 4096: 58 / 66 and
-// 69 / 73, 64 of 2048 x 2048: 44 / 65 and 54 / 57; mean 32: 83 / 73 and 65 / 58.  So up to a mean of 16.
-static bool few_rows(const GemmExtArgs& g) { return g.experts ? g.M <= (127 + 16) * g.experts + 127 : g.M <= 128; }
+// nvfp4_moe_rows, M / experts is about 127 more than the mean.  Mean 16, 32, 40 rows, the same two times:
+//   8 experts of 14336 x 4096    57 / 73   72 / 74   84 / 74
+//   64 experts of 2048 x 2048    36 / 57   45 / 55   49 / 55
+//   64 experts of 4096 x 1024    41 / 96   47 / 96   50 / 97
+//   16 experts of 4096 x 4096    34 / 46   45 / 47   47 / 47
+// so up to a mean of 32, which is one pass of that kernel.
+static bool few_rows(const GemmExtArgs& g) { return g.experts ? g.M <= (127 + 32) * g.experts + 127 : g.M <= 128; }
 
 static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {
     if (!g.a || !g.sfa || !g.a_gs || !g.b || !g.sfb || !g.b_gs || !g.c) return NVFP4_ERR_INVALID_ARG;

@@ -11,8 +11,13 @@
 //     meet in distributed shared memory, tokens dealt to the CTAs, and are
 //     added in the order of the CTAs: no workspace, no atomics, the same
 //     result every time.
-//   - Two CTAs to an SM, each with 72 KB (64 tokens and more: 54 KB) of weight
+//   - Two CTAs to an SM, each with 72 KB (more than 32 tokens: 54 KB) of weight
 //     in flight, several times what hides the latency of HBM.
+//   - Weights with more tiles than the GPU has SMs need no split: then a CTA
+//     streams through tiles (gemm_few_stream_kernel).
+// Measured in a chain (us, share of HBM's rate on the weight's bytes): one token
+// through 14336 x 4096 9.8 (0.51), 28672 x 8192 24.4 (0.83), 131072 x 4096 50
+// (0.91); 16 tokens x 2 through 8 experts of 14336 x 4096 56 (0.72).
 //   - Warp 0: TMA producer.  Warp 1: the MMAs.  Warps 2 .. 5: block scales to
 //     tensor memory (a copy by the tensor core, tcgen05.cp, costs its pipe 64
 //     cycles; with 8 of them a block of K = 256 took 1015 cycles instead of
@@ -188,6 +193,75 @@ __device__ __forceinline__ void finish(const FewParams& p, const Finish& f, int6
         if (e < f.count) amax = max(amax, __float_as_uint(fabsf(v[e])));
 }
 
+// One stage: K block kb of the weight tile at row w_row and of the tokens from t0.
+struct Source {
+    const uint8_t* sfw;
+    const uint8_t* sfx;
+    int w_row, t0, boxes;
+};
+template <int TOK>
+__device__ __forceinline__ void load_stage(uint32_t at, uint32_t full, const CUtensorMap& map_w, const CUtensorMap& map_x,
+                                           const Source& src, int kb, int nk) {
+    using L = Layout<TOK>;
+    mbar_expect_tx(full, (uint32_t)(F_W_STAGE + src.boxes * 16 * F_BKB + 2 * nk * 512));
+    tma_load_2d(at, &map_w, full, kb * F_BKB, src.w_row);
+    bulk_load(at + L::kOffSfw, src.sfw + (int64_t)kb * 2048, nk * 512, full);
+    for (int b = 0; b < src.boxes; ++b)
+        tma_load_2d(at + L::kOffX + b * 16 * F_BKB, &map_x, full, kb * F_BKB, src.t0 + 16 * b);
+    bulk_load(at + L::kOffSfx, src.sfx + (int64_t)kb * 2048, nk * 512, full);
+}
+__device__ __forceinline__ Source source(const FewParams& p, int e, int tile, int t0, int tokens) {
+    return Source{p.sfw + e * p.sfw_stride + (int64_t)tile * p.chunks_k * 512, p.sfx + (int64_t)(t0 >> 7) * p.chunks_k * 512,
+                  e * p.N + tile * F_ROWS, t0, (tokens + 15) / 16};
+}
+// A stage's block scales, shared memory -> this warp's lane quarter of tensor memory.  32 rows go to a column: a pass of
+// up to 32 tokens starts at the column of its rows in the chunk of 128.
+template <int TOK>
+__device__ __forceinline__ void scale_stage(uint32_t smem_scales, uint32_t taddr, int t0, int lane) {
+    const int quarter = (t0 >> 5) & 3;
+    uint32_t w[16], x[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 a = lds128(smem_scales + 16 * lane + 512 * j), b = lds128(smem_scales + F_SF_STAGE + 16 * lane + 512 * j);
+        w[4 * j] = a.x; w[4 * j + 1] = a.y; w[4 * j + 2] = a.z; w[4 * j + 3] = a.w;
+        x[4 * j] = TOK == 128 || quarter == 0 ? b.x : quarter == 1 ? b.y : quarter == 2 ? b.z : b.w;
+        x[4 * j + 1] = b.y; x[4 * j + 2] = b.z; x[4 * j + 3] = b.w;
+    }
+    tc_st_32x32b_x16(taddr, w);
+    tc_st_32x32b_x16(taddr + 16, x);
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+}
+__device__ __forceinline__ uint32_t few_idesc(int boxes) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(16 * boxes >> 3) << 17) | ((uint32_t)(F_ROWS >> 4) << 24);
+}
+__device__ __forceinline__ Finish finish_at(const FewParams& p, int e, int64_t n) {
+    Finish f;
+    f.n = n;
+    f.count = (int)min((int64_t)4, p.N - n);
+    const float sx = __ldg(p.x_gs), sw = __ldg(p.w_gs + e), a = __fmul_rn(sx, sw);
+    // as the large product: one factor, or two where it leaves the normal range
+    f.alpha = a >= 0x1p-126f && a <= 0x1.fffffep127f ? make_float2(a, 1.0f) : make_float2(sx, sw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f.bias[i] = p.bias && i < f.count ? __bfloat162float(p.bias[(int64_t)e * p.N + n + i]) : 0.0f;
+    return f;
+}
+// Rows without a token become zeros: the segment's behind `stop`, in this tile's columns.
+__device__ __forceinline__ void zero_padding(const FewParams& p, int e, int n0, int stop, int worker, int workers, int lane) {
+    const int esz = p.out_bf16 ? 2 : 4, cols = min(F_ROWS, p.N - n0);
+    const int end = max(segment_start(p.offsets, e + 1, p.M), stop);
+    zero_rows(static_cast<uint8_t*>(p.c) + (int64_t)n0 * esz, (int64_t)cols * esz, p.ldc * esz, stop, end, worker, workers, lane);
+    if (p.pre) zero_rows(p.pre + n0, cols * 2, p.ldp * 2, stop, end, worker, workers, lane);
+}
+// ... and all rows behind the last segment.
+__device__ __forceinline__ void zero_tail(const FewParams& p, int worker, int workers, int lane) {
+    const int esz = p.out_bf16 ? 2 : 4, tail = segment_start(p.offsets, p.experts, p.M);
+    zero_rows(p.c, (int64_t)p.N * esz, p.ldc * esz, tail, p.M, worker, workers, lane);
+    if (p.pre) zero_rows(p.pre, (int64_t)p.N * 2, p.ldp * 2, tail, p.M, worker, workers, lane);
+}
+
 template <int TOK, int ACT>
 __global__ void __launch_bounds__(F_THREADS, 2)
 gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, FewParams p) {
@@ -238,17 +312,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     if (L::kOwnSums && splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA runs
     const uint32_t tmem = *tmem_slot;
 
-    Finish f;
-    {
-        f.n = n0 + 4 * lane;
-        f.count = (int)min((int64_t)4, p.N - f.n);
-        const float sx = __ldg(p.x_gs), sw = __ldg(p.w_gs + e), a = __fmul_rn(sx, sw);
-        // as the large product: one factor, or two where it leaves the normal range
-        f.alpha = a >= 0x1p-126f && a <= 0x1.fffffep127f ? make_float2(a, 1.0f) : make_float2(sx, sw);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f.bias[i] = p.bias && i < f.count ? __bfloat162float(p.bias[(int64_t)e * p.N + f.n + i]) : 0.0f;
-    }
+    const Finish f = finish_at(p, e, n0 + 4 * lane);
     uint32_t amax = 0;
     int s = 0;                      // stage and its phase, of each role
     uint32_t phase = 0, acc_phase = 0;
@@ -258,18 +322,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
         if (warp == 0) {
             if (lane == 0) {
-                const uint8_t* sfw = p.sfw + e * p.sfw_stride + (int64_t)tile * p.chunks_k * 512;
-                const uint8_t* sfx = p.sfx + (int64_t)(t0 >> 7) * p.chunks_k * 512;
+                const Source src = source(p, e, tile, t0, tokens);
                 for (int kb = kb0; kb < kb1 && ok; ++kb) {
                     if (!mbar_wait(bar_empty + 8 * s, phase ^ 1, abort_flag)) { ok = false; break; }
-                    const int nk = min(4, steps - kb * 4);
-                    const uint32_t full = bar_full + 8 * s, at = sbase + s * L::kStage;
-                    mbar_expect_tx(full, (uint32_t)(F_W_STAGE + boxes * 16 * F_BKB + 2 * nk * 512));
-                    tma_load_2d(at, &map_w, full, kb * F_BKB, e * p.N + n0);
-                    bulk_load(at + L::kOffSfw, sfw + (int64_t)kb * 2048, nk * 512, full);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(at + L::kOffX + b * 16 * F_BKB, &map_x, full, kb * F_BKB, t0 + 16 * b);
-                    bulk_load(at + L::kOffSfx, sfx + (int64_t)kb * 2048, nk * 512, full);
+                    load_stage<TOK>(sbase + s * L::kStage, bar_full + 8 * s, map_w, map_x, src, kb, min(4, steps - kb * 4));
                     issued_any |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
                     if (++s == L::kStages) { s = 0; phase ^= 1; }
@@ -277,8 +333,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             }
         } else if (warp == 1) {
             if (lane == 0) {
-                const uint32_t idesc =
-                    (1u << 7) | (1u << 10) | ((uint32_t)(16 * boxes >> 3) << 17) | ((uint32_t)(F_ROWS >> 4) << 24);
+                const uint32_t idesc = few_idesc(boxes);
                 for (int kb = kb0; kb < kb1 && ok; ++kb) {
                     // raised by the scale warps once the stage had landed
                     if (!mbar_wait(bar_sf + 8 * s, phase, abort_flag)) { ok = false; break; }
@@ -292,24 +347,9 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             }
         } else {
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const int quarter = (t0 >> 5) & 3;
             for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                if (!mbar_wait(bar_full + 8 * s, phase, abort_flag)) { ok = false; break; }
-                const uint32_t sf = sbase + s * L::kStage + L::kOffSfw + 16 * lane;
-                uint32_t w[16], x[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 a = lds128(sf + 512 * j), b = lds128(sf + F_SF_STAGE + 512 * j);
-                    w[4 * j] = a.x; w[4 * j + 1] = a.y; w[4 * j + 2] = a.z; w[4 * j + 3] = a.w;
-                    // 32 rows to a column: a pass of up to 32 tokens starts at the column of its rows in the chunk of 128
-                    x[4 * j] = TOK == 128 || quarter == 0 ? b.x : quarter == 1 ? b.y : quarter == 2 ? b.z : b.w;
-                    x[4 * j + 1] = b.y; x[4 * j + 2] = b.z; x[4 * j + 3] = b.w;
-                }
-                tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32, w);
-                tc_st_32x32b_x16(tmem + lanes + L::kSf + s * 32 + 16, x);
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, phase, abort_flag))) { ok = false; break; }
+                scale_stage<TOK>(sbase + s * L::kStage + L::kOffSfw, tmem + lanes + L::kSf + s * 32, t0, lane);
                 if (lane == 0) mbar_arrive(bar_sf + 8 * s);
                 if (++s == L::kStages) { s = 0; phase ^= 1; }
             }
@@ -381,15 +421,8 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         if (lane == 0 && m) atomicMax(s_amax, m);
     }
     if (p.offsets && warp >= 2) {
-        // rows without a token: the segment's for these features, and those behind the last segment
-        const int esz = p.out_bf16 ? 2 : 4, worker = rank * 4 + warp - 2, all = gridDim.x * 4;
-        const int cols = min(F_ROWS, p.N - n0), end = max(segment_start(p.offsets, e + 1, p.M), stop);
-        uint8_t* c = static_cast<uint8_t*>(p.c) + (int64_t)n0 * esz;
-        zero_rows(c, (int64_t)cols * esz, p.ldc * esz, stop, end, worker, splits * 4, lane);
-        if (p.pre) zero_rows(p.pre + n0, cols * 2, p.ldp * 2, stop, end, worker, splits * 4, lane);
-        const int tail = segment_start(p.offsets, p.experts, p.M), me = blockIdx.x * 4 + warp - 2;
-        zero_rows(p.c, (int64_t)p.N * esz, p.ldc * esz, tail, p.M, me, all, lane);
-        if (p.pre) zero_rows(p.pre, (int64_t)p.N * 2, p.ldp * 2, tail, p.M, me, all, lane);
+        zero_padding(p, e, n0, stop, rank * 4 + warp - 2, splits * 4, lane);
+        zero_tail(p, blockIdx.x * 4 + warp - 2, gridDim.x * 4, lane);
     }
     // After an abort, no copy and no MMA may be in flight when memory is released; otherwise every copy was waited for by
     // the scale warps and every MMA by the accumulator's barrier.
@@ -417,7 +450,203 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     }
 }
 
+// The same where there is enough to do without splitting K: a CTA goes through
+// tiles (of features, per expert) one after the other, and the operands of the
+// next tiles are on their way while a finished one leaves.  Against a CTA per
+// tile: 8 experts of 14336 x 4096 71 -> 56 us, 64 of 2048 x 2048 54 -> 33, 64 of
+// 4096 x 1024 75 -> 38, one token through 131072 x 4096 57 -> 50.
+// Two accumulators; the epilogue has four warps of its own, each with its 32
+// features of 16 tokens at a time turned through 2 KB of shared memory.
+constexpr int S_THREADS = 320;
+template <int TOK>
+struct StreamLayout {
+    using L = Layout<TOK>;
+    static constexpr int kOffTurn = L::kStages * L::kStage;
+    static constexpr int kOffBar = kOffTurn + 4 * 2048;       // full, empty, scales per stage; 2 accumulators full, empty; drain
+    static constexpr int kOffMisc = kOffBar + (3 * L::kStages + 5) * 8;
+    static constexpr int kBytes = kOffMisc + 16 + 1008;
+    static constexpr uint32_t kSf = 2 * TOK;
+    static_assert(TOK <= 32 && kSf + L::kStages * 32 <= F_TMEM, "tensor memory");
+};
+
+template <int TOK, int ACT>
+__global__ void __launch_bounds__(S_THREADS, 2)
+gemm_few_stream_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, FewParams p) {
+    using L = Layout<TOK>;
+    using S = StreamLayout<TOK>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + S::kOffBar, bar_empty = bar_full + 8 * L::kStages;
+    const uint32_t bar_sf = bar_empty + 8 * L::kStages, bar_acc = bar_sf + 8 * L::kStages;
+    const uint32_t bar_free = bar_acc + 16, bar_drain = bar_free + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
+    unsigned int* s_amax = reinterpret_cast<unsigned int*>(smem + S::kOffMisc + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = p.tiles * p.experts, stride = gridDim.x;
+    const int steps = p.K / 64, blocks = (steps + 3) / 4;
+
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_x);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+            mbar_init(bar_sf + 8 * s, 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_acc + 8 * b, 1);
+            mbar_init(bar_free + 8 * b, 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        *s_amax = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(F_TMEM));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    wait_for_stream();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // Every role goes through the same tiles and passes.  A tile's rows are fetched one tile ahead: they are read from
+    // global memory, and nothing should wait for that between two tiles.
+    auto rows_of = [&](int unit, int& e, int& tile, int& start, int& stop) {
+        e = min(unit, units - 1) / p.tiles;
+        tile = min(unit, units - 1) - e * p.tiles;
+        start = p.offsets ? segment_start(p.offsets, e, p.M) : 0;
+        stop = p.offsets ? segment_end(p.offsets, p.counts, e, p.M) : p.M;
+    };
+    int e1, tile1, start1, stop1;
+    rows_of(blockIdx.x, e1, tile1, start1, stop1);
+    int s = 0, acc = 0;             // stage and accumulator, and their phases, of each role
+    uint32_t phase = 0, acc_phase = 0, amax = 0;
+    uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
+    bool ok = true;
+    if (p.offsets && warp >= 6) zero_tail(p, blockIdx.x * 4 + warp - 6, gridDim.x * 4, lane);
+    for (int unit = blockIdx.x; unit < units && ok; unit += stride) {
+        const int e = e1, tile = tile1, start = start1, stop = stop1, n0 = tile * F_ROWS;
+        rows_of(unit + stride, e1, tile1, start1, stop1);
+        Finish f;
+        if (warp >= 6) f = finish_at(p, e, n0 + 32 * (warp & 3) + 4 * (lane & 7));
+        for (int t0 = start; t0 < stop && ok; t0 += TOK) {
+            const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
+            if (warp == 0) {
+                if (lane == 0) {
+                    const Source src = source(p, e, tile, t0, tokens);
+                    for (int kb = 0; kb < blocks; ++kb) {
+                        if (!mbar_wait(bar_empty + 8 * s, phase ^ 1, abort_flag)) { ok = false; break; }
+                        load_stage<TOK>(sbase + s * L::kStage, bar_full + 8 * s, map_w, map_x, src, kb, min(4, steps - kb * 4));
+                        issued_any |= 1u << s;
+                        issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
+                        if (++s == L::kStages) { s = 0; phase ^= 1; }
+                    }
+                }
+            } else if (warp == 1) {
+                if (lane == 0) {
+                    ok = mbar_wait(bar_free + 8 * acc, acc_phase ^ 1, abort_flag);
+                    tc_fence_after();
+                    const uint32_t idesc = few_idesc(boxes);
+                    for (int kb = 0; kb < blocks && ok; ++kb) {
+                        if (!mbar_wait(bar_sf + 8 * s, phase, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        issue_steps<L::kOffX>(tmem + acc * TOK, (sbase + s * L::kStage) >> 4, tmem + S::kSf + s * 32, idesc,
+                                              min(4, steps - kb * 4), kb > 0);
+                        tc_commit(bar_empty + 8 * s);
+                        if (++s == L::kStages) { s = 0; phase ^= 1; }
+                    }
+                    if (ok) tc_commit(bar_acc + 8 * acc);
+                }
+            } else if (warp < 6) {
+                const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, phase, abort_flag))) { ok = false; break; }
+                    scale_stage<TOK>(sbase + s * L::kStage + L::kOffSfw, tmem + lanes + S::kSf + s * 32, t0, lane);
+                    if (lane == 0) mbar_arrive(bar_sf + 8 * s);
+                    if (++s == L::kStages) { s = 0; phase ^= 1; }
+                }
+            } else {
+                ok = mbar_wait(bar_acc + 8 * acc, acc_phase, abort_flag);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (ok) {
+                    tc_fence_after();
+                    uint32_t v[TOK / 16][16];
+#pragma unroll
+                    for (int b = 0; b < TOK / 16; ++b)
+                        tc_ld_32x32b_x16(tmem + acc * TOK + ((uint32_t)((warp & 3) * 32) << 16) + 16 * b, v[b]);
+                    tc_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_free + 8 * acc);
+                    float* turn = reinterpret_cast<float*>(smem + S::kOffTurn) + (warp & 3) * 512;   // [token][feature]
+#pragma unroll
+                    for (int b = 0; b < TOK / 16; ++b) {
+                        if (16 * b >= tokens) break;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) turn[32 * j + lane] = __uint_as_float(v[b][j]);
+                        __syncwarp();
+                        for (int t = 16 * b + (lane >> 3); t < min(tokens, 16 * b + 16); t += 4)
+                            finish<ACT>(p, f, t0 + t, *reinterpret_cast<const float4*>(turn + 32 * (t - 16 * b) + 4 * (lane & 7)), amax);
+                        __syncwarp();
+                    }
+                }
+            }
+            if (warp < 2) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        }
+        if (p.offsets && warp >= 6) zero_padding(p, e, n0, stop, warp - 6, 4, lane);
+    }
+    if (p.c_amax && warp >= 6) {
+        __syncwarp();
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, amax);
+        if (lane == 0 && m) atomicMax(s_amax, m);
+    }
+    // As above: after an abort, no copy and no MMA may be in flight when memory is released.
+    if (*abort_flag) {
+        if (warp == 0 && lane == 0) {
+            for (int st = 0; st < L::kStages; ++st)
+                if (issued_any & (1u << st)) {
+                    const unsigned long long w0 = globaltimer();
+                    while (!mbar_try(bar_full + 8 * st, (issued_parity >> st) & 1u) && globaltimer() - w0 < kWaitLimitNs) {}
+                }
+        }
+        if (warp == 1 && lane == 0) {
+            tc_commit(bar_drain);
+            const unsigned long long w0 = globaltimer();
+            while (!mbar_try(bar_drain, 0) && globaltimer() - w0 < kWaitLimitNs) {}
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (p.c_amax && threadIdx.x == 0 && *s_amax) atomicMax(p.c_amax, *s_amax);
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
+    }
+}
+
 typedef void (*FewKernel)(const CUtensorMap, const CUtensorMap, FewParams);
+
+template <int TOK>
+FewKernel stream_kernel(int act) {
+    switch (act) {
+        case ACT_RELU: return gemm_few_stream_kernel<TOK, ACT_RELU>;
+        case ACT_RELU2: return gemm_few_stream_kernel<TOK, ACT_RELU2>;
+        case ACT_GELU: return gemm_few_stream_kernel<TOK, ACT_GELU>;
+        case ACT_GELU_TANH: return gemm_few_stream_kernel<TOK, ACT_GELU_TANH>;
+        case ACT_SILU: return gemm_few_stream_kernel<TOK, ACT_SILU>;
+        default: return gemm_few_stream_kernel<TOK, ACT_NONE>;
+    }
+}
 
 template <int TOK>
 FewKernel few_kernel(int act) {
@@ -445,6 +674,8 @@ int prepared_sms() {
             cudaFuncSetAttribute(few_kernel<16>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<16>::kBytes);
             cudaFuncSetAttribute(few_kernel<32>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<32>::kBytes);
             cudaFuncSetAttribute(few_kernel<128>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kBytes);
+            cudaFuncSetAttribute(stream_kernel<16>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, StreamLayout<16>::kBytes);
+            cudaFuncSetAttribute(stream_kernel<32>(act), cudaFuncAttributeMaxDynamicSharedMemorySize, StreamLayout<32>::kBytes);
         }
         cached[dev] = n > 0 ? n : 148;
     }
@@ -486,6 +717,11 @@ cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
     int splits = 1;
     while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
     const int tokens = g.offsets ? 32 : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
+    if (splits == 1 && tokens <= 32) {
+        const int grid = (int)(units < 2 * sms ? units : 2 * sms);
+        return tokens == 16 ? launch_early(stream_kernel<16>(g.act), grid, S_THREADS, StreamLayout<16>::kBytes, s, 1, mw, mx, p)
+                            : launch_early(stream_kernel<32>(g.act), grid, S_THREADS, StreamLayout<32>::kBytes, s, 1, mw, mx, p);
+    }
     FewKernel kernel = tokens == 16 ? few_kernel<16>(g.act) : tokens == 32 ? few_kernel<32>(g.act) : few_kernel<128>(g.act);
     const int smem = tokens == 16 ? Layout<16>::kBytes : tokens == 32 ? Layout<32>::kBytes : Layout<128>::kBytes;
     return launch_early(kernel, (unsigned)(units * splits), F_THREADS, smem, s, splits, mw, mx, p);

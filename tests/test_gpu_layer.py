@@ -499,7 +499,7 @@ def test_products_with_nothing_routed(rows):
     assert all((x == 0).all() for x in (out, pre, dw, dz, db)) and amax.item() == 0
 
 
-@pytest.mark.parametrize("experts,count", [(1, 40), (2, 100), (3, 129), (16, 33)])
+@pytest.mark.parametrize("experts,count", [(1, 40), (2, 100), (3, 129), (16, 33), (70, 5)])
 def test_grouped_kernels_agree_where_the_choice_changes(experts, count):
     """The same rows with a row capacity just below and above the one that decides between the two kernels."""
     Nn, K = 264, 320
@@ -509,7 +509,7 @@ def test_grouped_kernels_agree_where_the_choice_changes(experts, count):
     b = (torch.stack([w.codes for w in q]), torch.stack([w.scales_mma for w in q]), torch.cat([w.global_scale for w in q]))
     got = []
     need = experts * ((count + 127) // 128 * 128)
-    for rows in (need, 143 * experts + 255 + need):
+    for rows in (need, 160 * experts + 255 + need):
         plan = N.moe_sort(ids.contiguous(), experts, rows=rows // 128 * 128)
         a = N.quantize_1d(N.moe_gather(x, plan))
         c = N.gemm_grouped(*quant_args(a), *b, plan, plan.rows, Nn, K, bias=bf16(experts, Nn, seed=43),
