@@ -41,6 +41,7 @@ EXPORTS = (
 )
 
 _lib = None
+_current_device = torch._C._cuda_getDevice
 
 
 class Nvfp4Error(RuntimeError):
@@ -138,7 +139,7 @@ def _p(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:   # the current stream's handle, without building a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -497,9 +498,11 @@ def quantize_dual(x: torch.Tensor, rounding: int = NVFP4_RNE, sr_seed: int = 0, 
 
 
 # ------------------------------------------------------ the linear layer ----
-def _here(t: torch.Tensor):
+def _here(*tensors: torch.Tensor):
     """Launches go to the current device: a tensor elsewhere (host memory included) is refused."""
-    assert t.get_device() == torch._C._cuda_getDevice(), f"tensor on {t.device}, not on the current CUDA device"
+    dev = _current_device()
+    for t in tensors:
+        assert t.get_device() == dev, f"tensor on {t.device}, not on the current CUDA device"
 
 
 def _matrix(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> int:
@@ -536,8 +539,7 @@ def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
     need = (rows + 127) // 128 * ((k // 16 + 3) // 4) * 512      # nvfp4_mma_scale_bytes
     assert scales_mma.numel() >= experts * need and scales_mma.is_contiguous()
     assert gs.dtype is torch.float32 and gs.numel() == experts and gs.is_contiguous()
-    for t in (codes, scales_mma, gs):
-        _here(t)
+    _here(codes, scales_mma, gs)
 
 
 def _check_word(t):

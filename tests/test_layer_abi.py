@@ -151,7 +151,7 @@ def test_row_movements(L):
 def test_helpers_refuse_mismatched_tensors(monkeypatch):
     """The torch helpers check shapes and types before they hand out pointers (CPU tensors stand in)."""
     u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
-    monkeypatch.setattr(N, "_here", lambda t: None)      # the device check has a test of its own
+    monkeypatch.setattr(N, "_here", lambda *t: None)     # the device check has a test of its own
     f = torch.zeros(1)
     plan = N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 2, 256, (8, 2))))
     assert (plan.experts, plan.rows, plan.tokens, plan.topk) == (2, 256, 8, 2)
@@ -180,7 +180,7 @@ def test_helpers_refuse_mismatched_tensors(monkeypatch):
 
 def test_helpers_refuse_tensors_that_are_not_on_the_current_device(monkeypatch):
     """Host tensors stand for those of another device: either would hand the kernels addresses they cannot read."""
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(N, "_current_device", lambda: 0)
     u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
     plan = N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 2, 256, (8, 2))))
