@@ -359,7 +359,8 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
  *
  * nvfp4_gemm_epilogue:
  *   z = alpha A . B^T + bias,   C = act(z) + residual
- *   Operands, shapes, alpha, C and alignment as nvfp4_gemm; M from 1.
+ *   Operands, shapes, alpha, C and alignment as nvfp4_gemm; M from 1
+ *   (up to 128 rows, and experts with few rows, have a kernel of their own).
  *   bias       bf16 [N] (2-byte aligned), nullable.
  *   activation one of NVFP4_ACT_*.
  *   residual   bf16 [M x ldr], nullable; ldr >= N a multiple of 8, 16-byte

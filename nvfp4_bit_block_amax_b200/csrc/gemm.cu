@@ -28,6 +28,10 @@
 //   warps 6..9  epilogue of columns 128..255.  Epilogue: TMEM -> registers
 //               (128 columns per thread, packed to bf16), free the
 //               accumulator for the next tile, then scale by alpha and store.
+// The pair kernel (below) is the default.  It also computes the linear layer's
+// product with its epilogue, the same over rows sorted by expert, and the
+// experts' weight gradients: modes of one template, with the same operand path
+// and an epilogue of their own.
 // Every mbarrier wait is bounded in time: on expiry the kernel raises the
 // device error word, lets in-flight copies and MMAs land, frees TMEM and
 // returns (nvfp4_get_error reports NVFP4_ERR_TIMEOUT).

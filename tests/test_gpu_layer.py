@@ -108,7 +108,8 @@ def ok():
 
 # ---------------------------------------------------------------- epilogue --
 SHAPES = [(1, 64, 64), (1, 4100, 1024), (3, 130, 192), (8, 8, 64), (17, 1000, 4160), (33, 520, 320), (64, 264, 8192),
-          (65, 129, 128), (128, 256, 256), (129, 1024, 1088), (300, 200, 832), (513, 1, 64)]
+          (65, 129, 128), (128, 256, 256), (129, 1024, 1088), (300, 200, 832), (513, 1, 64),
+          (5, 40000, 320), (20, 40008, 64), (100, 20000, 256)]     # more tiles than there are CTAs
 
 
 @pytest.mark.parametrize("M,Nn,K", SHAPES)
@@ -415,7 +416,8 @@ def test_gather_and_combine_are_each_others_gradient():
 
 # ---------------------------------------------------------------- experts ---
 EXPERTS = [(1, 1, 1, 64, 64), (16, 2, 8, 264, 128), (5, 2, 3, 1000, 320), (300, 2, 4, 520, 192), (700, 3, 5, 256, 1088),
-           (100, 1, 40, 130, 64), (2000, 4, 16, 384, 512)]
+           (100, 1, 40, 130, 64), (2000, 4, 16, 384, 512),
+           (90, 2, 128, 520, 64)]
 
 
 def expert_operands(tokens, topk, experts, Nn, K, seed, bad=0.0):
