@@ -532,77 +532,100 @@ gemm_few_stream_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
     bool ok = true;
     if (p.offsets && warp >= 6) zero_tail(p, blockIdx.x * 4 + warp - 6, gridDim.x * 4, lane);
-    for (int unit = blockIdx.x; unit < units && ok; unit += stride) {
-        const int e = e1, tile = tile1, start = start1, stop = stop1, n0 = tile * F_ROWS;
-        rows_of(unit + stride, e1, tile1, start1, stop1);
+    auto pass = [&](int e, int tile, int t0, int stop) {
         Finish f;
-        if (warp >= 6) f = finish_at(p, e, n0 + 32 * (warp & 3) + 4 * (lane & 7));
-        for (int t0 = start; t0 < stop && ok; t0 += TOK) {
-            const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
-            if (warp == 0) {
-                if (lane == 0) {
-                    const Source src = source(p, e, tile, t0, tokens);
-                    for (int kb = 0; kb < blocks; ++kb) {
-                        if (!mbar_wait(bar_empty + 8 * s, phase ^ 1, abort_flag)) { ok = false; break; }
-                        load_stage<TOK>(sbase + s * L::kStage, bar_full + 8 * s, map_w, map_x, src, kb, min(4, steps - kb * 4));
-                        issued_any |= 1u << s;
-                        issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
-                        if (++s == L::kStages) { s = 0; phase ^= 1; }
-                    }
-                }
-            } else if (warp == 1) {
-                if (lane == 0) {
-                    ok = mbar_wait(bar_free + 8 * acc, acc_phase ^ 1, abort_flag);
-                    tc_fence_after();
-                    const uint32_t idesc = few_idesc(boxes);
-                    for (int kb = 0; kb < blocks && ok; ++kb) {
-                        if (!mbar_wait(bar_sf + 8 * s, phase, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
-                        issue_steps<L::kOffX>(tmem + acc * TOK, (sbase + s * L::kStage) >> 4, tmem + S::kSf + s * 32, idesc,
-                                              min(4, steps - kb * 4), kb > 0);
-                        tc_commit(bar_empty + 8 * s);
-                        if (++s == L::kStages) { s = 0; phase ^= 1; }
-                    }
-                    if (ok) tc_commit(bar_acc + 8 * acc);
-                }
-            } else if (warp < 6) {
-                const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        if (warp >= 6) f = finish_at(p, e, tile * F_ROWS + 32 * (warp & 3) + 4 * (lane & 7));
+        const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
+        if (warp == 0) {
+            if (lane == 0) {
+                const Source src = source(p, e, tile, t0, tokens);
                 for (int kb = 0; kb < blocks; ++kb) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, phase, abort_flag))) { ok = false; break; }
-                    scale_stage<TOK>(sbase + s * L::kStage + L::kOffSfw, tmem + lanes + S::kSf + s * 32, t0, lane);
-                    if (lane == 0) mbar_arrive(bar_sf + 8 * s);
+                    if (!mbar_wait(bar_empty + 8 * s, phase ^ 1, abort_flag)) { ok = false; break; }
+                    load_stage<TOK>(sbase + s * L::kStage, bar_full + 8 * s, map_w, map_x, src, kb, min(4, steps - kb * 4));
+                    issued_any |= 1u << s;
+                    issued_parity = (issued_parity & ~(1u << s)) | (phase << s);
                     if (++s == L::kStages) { s = 0; phase ^= 1; }
                 }
-            } else {
-                ok = mbar_wait(bar_acc + 8 * acc, acc_phase, abort_flag);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (ok) {
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                ok = mbar_wait(bar_free + 8 * acc, acc_phase ^ 1, abort_flag);
+                tc_fence_after();
+                const uint32_t idesc = few_idesc(boxes);
+                for (int kb = 0; kb < blocks && ok; ++kb) {
+                    if (!mbar_wait(bar_sf + 8 * s, phase, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    uint32_t v[TOK / 16][16];
+                    issue_steps<L::kOffX>(tmem + acc * TOK, (sbase + s * L::kStage) >> 4, tmem + S::kSf + s * 32, idesc,
+                                          min(4, steps - kb * 4), kb > 0);
+                    tc_commit(bar_empty + 8 * s);
+                    if (++s == L::kStages) { s = 0; phase ^= 1; }
+                }
+                if (ok) tc_commit(bar_acc + 8 * acc);
+            }
+        } else if (warp < 6) {
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            for (int kb = 0; kb < blocks; ++kb) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, phase, abort_flag))) { ok = false; break; }
+                scale_stage<TOK>(sbase + s * L::kStage + L::kOffSfw, tmem + lanes + S::kSf + s * 32, t0, lane);
+                if (lane == 0) mbar_arrive(bar_sf + 8 * s);
+                if (++s == L::kStages) { s = 0; phase ^= 1; }
+            }
+        } else {
+            ok = mbar_wait(bar_acc + 8 * acc, acc_phase, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                tc_fence_after();
+                uint32_t v[TOK / 16][16];
 #pragma unroll
-                    for (int b = 0; b < TOK / 16; ++b)
-                        tc_ld_32x32b_x16(tmem + acc * TOK + ((uint32_t)((warp & 3) * 32) << 16) + 16 * b, v[b]);
-                    tc_wait_ld();
-                    tc_fence_before();
+                for (int b = 0; b < TOK / 16; ++b)
+                    tc_ld_32x32b_x16(tmem + acc * TOK + ((uint32_t)((warp & 3) * 32) << 16) + 16 * b, v[b]);
+                tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_free + 8 * acc);
+                float* turn = reinterpret_cast<float*>(smem + S::kOffTurn) + (warp & 3) * 512;   // [token][feature]
+#pragma unroll
+                for (int b = 0; b < TOK / 16; ++b) {
+                    if (16 * b >= tokens) break;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) turn[32 * j + lane] = __uint_as_float(v[b][j]);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_free + 8 * acc);
-                    float* turn = reinterpret_cast<float*>(smem + S::kOffTurn) + (warp & 3) * 512;   // [token][feature]
-#pragma unroll
-                    for (int b = 0; b < TOK / 16; ++b) {
-                        if (16 * b >= tokens) break;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) turn[32 * j + lane] = __uint_as_float(v[b][j]);
-                        __syncwarp();
-                        for (int t = 16 * b + (lane >> 3); t < min(tokens, 16 * b + 16); t += 4)
-                            finish<ACT>(p, f, t0 + t, *reinterpret_cast<const float4*>(turn + 32 * (t - 16 * b) + 4 * (lane & 7)), amax);
-                        __syncwarp();
-                    }
+                    for (int t = 16 * b + (lane >> 3); t < min(tokens, 16 * b + 16); t += 4)
+                        finish<ACT>(p, f, t0 + t, *reinterpret_cast<const float4*>(turn + 32 * (t - 16 * b) + 4 * (lane & 7)), amax);
+                    __syncwarp();
                 }
             }
-            if (warp < 2) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
-        if (p.offsets && warp >= 6) zero_padding(p, e, n0, stop, warp - 6, 4, lane);
+        if (warp < 2) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    };
+    for (int unit = blockIdx.x; unit < units && ok; unit += stride) {
+        const int e = e1, tile = tile1, start = start1, stop = stop1;
+        rows_of(unit + stride, e1, tile1, start1, stop1);
+        if (start < stop) pass(e, tile, start, stop);
+        if (p.offsets && warp >= 6) zero_padding(p, e, tile * F_ROWS, stop, warp - 6, 4, lane);
+    }
+    // Experts with more rows than one pass takes: their other passes, dealt to all CTAs, so that an expert which got most
+    // of the tokens does not leave the GPU to a few of them (all of 1024 tokens to one of 64 experts of 2048 x 2048: 125 -> 19 us).
+    if (p.offsets) {
+        int next = units % stride;      // the CTA whose turn it is
+        for (int base = 0; base < p.experts && ok; base += 32) {
+            int first = 0, last = 0;
+            if (base + lane < p.experts) {
+                first = segment_start(p.offsets, base + lane, p.M);
+                last = segment_end(p.offsets, p.counts, base + lane, p.M);
+            }
+            unsigned more = __ballot_sync(0xFFFFFFFFu, last - first > TOK);
+            while (more && ok) {
+                const int from = __ffs(more) - 1;
+                more &= more - 1;
+                const int start = __shfl_sync(0xFFFFFFFFu, first, from), stop = __shfl_sync(0xFFFFFFFFu, last, from);
+                const int64_t count = (int64_t)((stop - start + TOK - 1) / TOK - 1) * p.tiles;
+                for (int64_t i = ((int)blockIdx.x - next + stride) % stride; i < count && ok; i += stride)
+                    pass(base + from, (int)(i % p.tiles), start + (int)(i / p.tiles + 1) * TOK, stop);
+                next = (int)((next + count) % stride);
+            }
+        }
     }
     if (p.c_amax && warp >= 6) {
         __syncwarp();

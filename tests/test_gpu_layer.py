@@ -461,6 +461,33 @@ def test_grouped(tokens, topk, experts, Nn, K, act, dtype, full):
     assert (out[:, Nn:] == 7.0).all()
 
 
+@pytest.mark.parametrize("experts,tokens,share", [(40, 300, 1), (40, 700, 2), (3, 90, 1), (200, 1000, 3)])
+def test_grouped_with_most_rows_at_one_expert(experts, tokens, share):
+    """Every share-th token goes to one expert, the others in turn: many passes for one segment, none or one for the
+    others, in the kernel for few rows."""
+    K = 128
+    ids = (torch.arange(tokens, device="cuda", dtype=torch.int32) * 7) % experts
+    ids[::share] = experts - 1
+    plan = N.moe_sort(ids[:, None].contiguous(), experts)
+    a = N.quantize_1d(N.moe_gather(bf16(tokens, K, seed=51), plan))
+    w = N.quantize_1d(bf16(experts * 256, K, seed=52))       # 256 rows each, so that the scales divide by expert
+    gs = w.global_scale.repeat(experts)
+    pre = torch.full((plan.rows, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    c = N.gemm_grouped(*quant_args(a), w.codes, w.scales_mma, gs, plan, plan.rows, 256, K, out_dtype=N.NVFP4_OUT_F32,
+                       pre=pre)
+    ok()
+    av, wv = values64(a.codes, a.scales, a.global_scale), values64(w.codes, w.scales, w.global_scale)
+    copy = plan.row_copy.long()
+    e = ids.long()[copy.clamp_min(0)]
+    want = torch.einsum("rk,rnk->rn", av, wv.reshape(experts, 256, K)[e])
+    S = torch.einsum("rk,rnk->rn", av.abs(), wv.abs().reshape(experts, 256, K)[e])
+    live = (copy >= 0)[:, None]
+    want, S = torch.where(live, want, 0.0), torch.where(live, S, 0.0)
+    within(c, want, z_bound(K, S) + want.abs() * 2.0 ** -23)
+    within(pre, want, z_bound(K, S) + (want.abs() + z_bound(K, S)) * step(torch.bfloat16))
+    assert (c[~live[:, 0]] == 0).all() and (pre[~live[:, 0]] == 0).all()
+
+
 @pytest.mark.parametrize("tokens,topk,experts,M,Nn,dtype", [
     (1, 1, 1, 64, 64, torch.float32), (16, 2, 8, 264, 136, torch.bfloat16), (300, 2, 5, 40, 520, torch.float32),
     (700, 3, 40, 136, 64, torch.float32), (3000, 2, 4, 512, 256, torch.bfloat16)])
