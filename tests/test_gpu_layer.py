@@ -417,7 +417,7 @@ def test_gather_and_combine_are_each_others_gradient():
 # ---------------------------------------------------------------- experts ---
 EXPERTS = [(1, 1, 1, 64, 64), (16, 2, 8, 264, 128), (5, 2, 3, 1000, 320), (300, 2, 4, 520, 192), (700, 3, 5, 256, 1088),
            (100, 1, 40, 130, 64), (2000, 4, 16, 384, 512),
-           (90, 2, 128, 520, 64)]
+           (90, 2, 128, 520, 64), (40, 2, 3, 264, 1088), (90, 1, 2, 130, 2112), (60, 1, 1, 300, 4160)]
 
 
 def expert_operands(tokens, topk, experts, Nn, K, seed, bad=0.0):
