@@ -240,7 +240,7 @@ __device__ __forceinline__ Finish finish_at(const FewParams& p, int e, int64_t n
     Finish f;
     f.n = n;
     f.count = (int)min((int64_t)4, p.N - n);
-    const float sx = __ldg(p.x_gs), sw = __ldg(p.w_gs + e), a = __fmul_rn(sx, sw);
+    const float sx = *p.x_gs, sw = p.w_gs[e], a = __fmul_rn(sx, sw);
     // as the large product: one factor, or two where it leaves the normal range
     f.alpha = a >= 0x1p-126f && a <= 0x1.fffffep127f ? make_float2(a, 1.0f) : make_float2(sx, sw);
 #pragma unroll

@@ -152,7 +152,7 @@ __device__ __forceinline__ uint32_t packed_row_amax(const uint32_t (&packed)[64]
 // in range wherever C itself does.  MXFP4 operands have no global scale.
 __device__ __forceinline__ float2 out_scales(const KParams& p, int e = 0) {
     if (!p.a_gs) return make_float2(1.0f, 1.0f);
-    const float sa = __ldg(p.a_gs), sb = __ldg(p.b_gs + e);
+    const float sa = *p.a_gs, sb = p.b_gs[e];
     const float alpha = __fmul_rn(sa, sb);
     if (alpha >= 0x1p-126f && alpha <= 0x1.fffffep127f) return make_float2(alpha, 1.0f);
     return make_float2(sa, sb);

@@ -8,6 +8,11 @@
 // waiting CTA never keeps one out that it waits for.  A kernel ends after the
 // one it waited for, so the order of the stream holds along a chain, and in a
 // captured graph as well.  Chains of small kernels gain 2 to 4 us a step.
+//
+// Such a kernel reads global memory with ordinary loads alone.  The read-only
+// path (__ldg, ld.global.nc, const __restrict__) wants memory that nobody
+// writes as long as the kernel lives, and here the kernel ahead may be writing
+// it still; the compiler may also move such a load ahead of the wait.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -25,7 +25,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// 16-byte load of data that may be overwritten in place by the same thread.
+// 16-byte load of data that the kernel ahead may have written (see launch.cuh)
+// or that the same thread may overwrite in place.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -106,11 +107,11 @@ __device__ __forceinline__ int64_t live_rows(const int* offsets, const int* coun
     int lo = 0, hi = experts;   // last entry with offsets[lo] <= m0
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(offsets + mid) <= m0) lo = mid;
+        if (offsets[mid] <= m0) lo = mid;
         else hi = mid - 1;
     }
     if (lo >= experts) return m0;
-    const int64_t end = min((int64_t)__ldg(offsets + lo) + __ldg(counts + lo), (int64_t)__ldg(offsets + lo + 1));
+    const int64_t end = min((int64_t)offsets[lo] + counts[lo], (int64_t)offsets[lo + 1]);
     return max(m0, min(end, M));
 }
 
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
 // dbias [experts x N] from the sums of the row tiles: 64 columns per CTA, the
 // tiles of a segment dealt to 4 threads per column, then added in order.  With
 // `amax`, one more CTA takes the maximum of the first kernel's CTAs.
-__global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __restrict__ sums, int64_t M, int64_t N,
+__global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* sums, int64_t M, int64_t N,
                                                              int tile_rows, const int* offsets, const int* counts, float* dbias,
                                                              const uint32_t* maxima, int n_maxima, float* amax) {
     __shared__ float s[4][64];
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __rest
         if (blockIdx.y) return;
         uint32_t m = 0;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < n_maxima; i += kThreads) m = max(m, __ldg(maxima + i));
+        for (int i = threadIdx.x; i < n_maxima; i += kThreads) m = max(m, maxima[i]);
         m = cta_max(m);
         if (threadIdx.x == 0) *amax = __uint_as_float(m);
         return;
@@ -218,15 +219,15 @@ __global__ void __launch_bounds__(kThreads) bias_grad_kernel(const float* __rest
     const int64_t tiles = (M + tile_rows - 1) / tile_rows;
     int64_t first = 0, last = tiles;
     if (offsets) {
-        const int64_t o = __ldg(offsets + e);
-        const int64_t end = min(o + __ldg(counts + e), (int64_t)__ldg(offsets + e + 1));
+        const int64_t o = offsets[e];
+        const int64_t end = min(o + counts[e], (int64_t)offsets[e + 1]);
         first = max(o, (int64_t)0) / tile_rows;
         last = min(tiles, (end + tile_rows - 1) / tile_rows);
     }
     float t = 0.0f;
     if (col < N) {
 #pragma unroll 8
-        for (int64_t i = first + part; i < last; i += 4) t += __ldg(sums + i * N + col);
+        for (int64_t i = first + part; i < last; i += 4) t += sums[i * N + col];
     }
     s[part][c] = t;
     __syncthreads();
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(SortParams p) {
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.n);
     for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-        const int e = __ldg(p.ids + i);
+        const int e = p.ids[i];
         if (e >= 0 && e < p.experts) atomicAdd(s_count + e, 1);
     }
     __syncthreads();
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(SortParams p) {
     const int part = p.chunk / kWarps;
     const int64_t wb = begin + (int64_t)warp * part, we = min(wb + part, end);
     for (int64_t i = wb + lane; i < we; i += 32) {
-        const int e = __ldg(p.ids + i);
+        const int e = p.ids[i];
         if (e >= 0 && e < p.experts) atomicAdd(s_at + warp * p.experts + e, 1);
     }
     __syncthreads();
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(SortParams p) {
             } else {
 #pragma unroll 4
                 for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int h = __ldg(p.hist + (int64_t)b * p.experts + e);
+                    const int h = p.hist[(int64_t)b * p.experts + e];
                     total += h;
                     if (b < (int)blockIdx.x) before += h;
                 }
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(SortParams p) {
     // place the copies
     for (int64_t i0 = wb; i0 < we; i0 += 32) {
         const int64_t i = i0 + lane;
-        const int e = i < we ? __ldg(p.ids + i) : -1;
+        const int e = i < we ? p.ids[i] : -1;
         const bool ok = e >= 0 && e < p.experts;
         const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? e : -1);
         int row = -1;
@@ -373,7 +374,7 @@ struct MoveParams {
 };
 
 __device__ __forceinline__ int row_of(const MoveParams& p, int64_t copy) {
-    const int r = __ldg(p.copy_row + copy);
+    const int r = p.copy_row[copy];
     return r >= 0 && r < p.rows ? r : -1;
 }
 
@@ -388,7 +389,7 @@ __device__ __forceinline__ void zero_unit(const MoveParams& p, int64_t unit, int
     const int64_t r0 = unit % groups * kZeroRows, c0 = unit / groups * 1024;
     bool empty = false;
     if (lane < kZeroRows && r0 + lane < p.rows) {
-        const int c = __ldg(p.row_copy + r0 + lane);
+        const int c = p.row_copy[r0 + lane];
         empty = c < 0 || c >= p.tokens * p.topk;
     }
     unsigned todo = __ballot_sync(0xFFFFFFFFu, empty);
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(MoveParams p) {
         uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[i] = c0 + 256 * i < p.cols ? ldg_stream(p.src + t * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
+            v[i] = c0 + 256 * i < p.cols ? ld_stream(p.src + t * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
         bool used = false;
         for (int j = 0; j < p.topk; ++j) {
             const int r = row_of(p, t * p.topk + j);
@@ -461,14 +462,17 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(MoveParams p) {
         for (int j0 = 0; j0 < p.topk; j0 += COPIES) {
             uint4 v[COPIES][VECS];
             float w[COPIES];
+            int r[COPIES];
 #pragma unroll
             for (int j = 0; j < COPIES; ++j) {
-                const int r = j0 + j < p.topk ? row_of(p, t * p.topk + j0 + j) : -1;
-                w[j] = r < 0 ? 0.0f : p.weights ? __ldg(p.weights + t * p.topk + j0 + j) : 1.0f;
+                r[j] = j0 + j < p.topk ? row_of(p, t * p.topk + j0 + j) : -1;
+                w[j] = r[j] < 0 ? 0.0f : p.weights ? p.weights[t * p.topk + j0 + j] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < COPIES; ++j)
 #pragma unroll
                 for (int i = 0; i < VECS; ++i)
-                    v[j][i] = r >= 0 && in[i] ? ldg_stream(p.src + r * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
-            }
+                    v[j][i] = r[j] >= 0 && in[i] ? ld_stream(p.src + r[j] * p.lds + c0 + 256 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int j = 0; j < COPIES; ++j)
 #pragma unroll
@@ -525,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 4) combine_grad_kernel(MoveParams p)
 #pragma unroll
         for (int j = 0; j < kDots; ++j) {
             row[j] = j < m ? row_of(p, copy0 + j) : -1;
-            w[j] = j < m && p.weights ? __ldg(p.weights + copy0 + j) : 1.0f;
+            w[j] = j < m && p.weights ? p.weights[copy0 + j] : 1.0f;
             dot[j] = 0.0f;
         }
         for (int64_t c = 8 * (sub * 32 + lane); c < p.cols; c += 8 * 32 * WARPS) {
-            const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.src + t * p.lds + c));
+            const uint4 g = *reinterpret_cast<const uint4*>(p.src + t * p.lds + c);
             uint4 y[kDots];
 #pragma unroll
             for (int j = 0; j < kDots; ++j)
-                if (dots && row[j] >= 0) y[j] = ldg_stream(p.other + row[j] * p.ldo + c);
+                if (dots && row[j] >= 0) y[j] = ld_stream(p.other + row[j] * p.ldo + c);
             float f[8];
             unpack8(g, f);
 #pragma unroll

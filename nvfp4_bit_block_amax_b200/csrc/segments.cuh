@@ -11,11 +11,11 @@
 namespace nvfp4 {
 
 __device__ __forceinline__ int segment_start(const int* offsets, int e, int limit) {
-    return min(max(__ldg(offsets + e), 0), limit) & ~127;
+    return min(max(offsets[e], 0), limit) & ~127;
 }
 __device__ __forceinline__ int segment_end(const int* offsets, const int* counts, int e, int limit) {   // of the rows in use
     const int start = segment_start(offsets, e, limit);
-    return start + min(max(__ldg(counts + e), 0), max(segment_start(offsets, e + 1, limit) - start, 0));
+    return start + min(max(counts[e], 0), max(segment_start(offsets, e + 1, limit) - start, 0));
 }
 
 // Rows first .. last-1 of a matrix become zeros, one warp to a row; the rows
