@@ -592,7 +592,9 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_
     """(dz, dbias) of C = act(z) + residual with z = product + bias: dz = dy * act'(z) in bf16, dbias its column
     sums in fp32 ([N], with a plan [experts x N]; None without bias_grad).  z is the `pre` of gemm_epilogue."""
     M, N = dy.shape
-    assert plan is None or plan.rows == M
+    if plan is not None:
+        assert plan.rows == M
+        _here(plan.counts)
     ldy = _matrix(dy, M, N)
     ldz = _matrix(z, M, N) if z is not None else 0
     if out is None:
