@@ -8,10 +8,15 @@ fallback of any kind -- if the library cannot be loaded, calls raise.
 
 The lower-case helpers (``quantize_1d`` ...) only allocate the outputs with
 torch (PyTorch is used for device memory and streams) and call the C ABI.
+With ``stream`` (a torch stream or a handle) a helper allocates and launches
+there; its tensors may be dropped on either stream at any time.  What orders
+the two streams, as ever, is the caller's wait on one for the other.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -345,6 +350,47 @@ def nvfp4_selftest_wait_timeout(limit_ns: int, stream=None) -> int:
 
 
 # --------------------------------------------------------- torch helpers ----
+def _tensors(*values):
+    """The tensors among values, those in a Quantized, a MoePlan or a tuple included."""
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, tuple):
+            yield from _tensors(*v)
+        elif isinstance(v, (Quantized, MoePlan)):
+            yield from _tensors(*vars(v).values())
+
+
+def _torch_stream(stream):
+    if not isinstance(stream, int):
+        return stream
+    # 0 and 1 are the default stream's handles
+    return torch.cuda.ExternalStream(stream) if stream > 1 else torch.cuda.default_stream()
+
+
+def _on_stream(helper):
+    """A helper whose `stream` is made the current one while it runs, so that what it allocates belongs to the stream
+    that works on it.  The results are used by the caller's stream as well, and the arguments by `stream`: neither
+    goes back to the allocator before both are past them."""
+    at = list(inspect.signature(helper).parameters).index("stream")
+
+    @functools.wraps(helper)
+    def call(*args, **kw):
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return helper(*args, **kw)
+        here, there = torch.cuda.current_stream(), _torch_stream(stream)
+        with torch.cuda.stream(there):
+            result = helper(*args, **kw)
+        if here.cuda_stream != there.cuda_stream:
+            for t in _tensors(*args, *kw.values()):
+                t.record_stream(there)
+            for t in _tensors(result):
+                t.record_stream(here)
+        return result
+    return call
+
+
 @dataclass
 class Quantized:
     """One NVFP4 tensor Q [rows x cols] on the device."""
@@ -377,6 +423,7 @@ def _empty_u8(n, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def quantize_1d(x: torch.Tensor, transpose: bool = False, rounding: int = NVFP4_RNE, sr_seed: int = 0,
                 rht: bool = False, rht_seed: int = 0, plain_scales: bool = True, mma_scales: bool = True,
                 stream=None, amax: Optional[torch.Tensor] = None, rht_order: int = 16) -> Quantized:
@@ -408,6 +455,7 @@ def quantize_1d(x: torch.Tensor, transpose: bool = False, rounding: int = NVFP4_
     return Quantized(codes, scales, smma, gs, qr, qc)
 
 
+@_on_stream
 def quantize_2d(w: torch.Tensor, columnwise: bool = True, plain_scales: bool = True, mma_scales: bool = True,
                 stream=None, amax: Optional[torch.Tensor] = None) -> Quantized:
     """Quantize a bf16 weight with 16x16 tiles (rowwise codes, optional columnwise copy)."""
@@ -428,6 +476,7 @@ def quantize_2d(w: torch.Tensor, columnwise: bool = True, plain_scales: bool = T
     return Quantized(cr, sc, mr, gs, rows, cols, codes_col=cc, scales_mma_col=mc)
 
 
+@_on_stream
 def dequantize(q: Quantized, scale_mode: int = NVFP4_SCALE_1D, out_dtype: int = NVFP4_OUT_F32,
                stream=None) -> torch.Tensor:
     dt = torch.float32 if out_dtype == NVFP4_OUT_F32 else torch.bfloat16
@@ -436,6 +485,7 @@ def dequantize(q: Quantized, scale_mode: int = NVFP4_SCALE_1D, out_dtype: int = 
     return out
 
 
+@_on_stream
 def gemm(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: int, K: int,
          out_dtype: int = NVFP4_OUT_BF16, out: Optional[torch.Tensor] = None, stream=None,
          amax_out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -454,6 +504,7 @@ def gemm(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: in
     return out
 
 
+@_on_stream
 def mxfp4_quantize(x: torch.Tensor, plain_scales: bool = True, mma_scales: bool = True, stream=None) -> Quantized:
     """MXFP4 quantization of a bf16 [rows x cols] tensor (32-element blocks, E8M0 scales)."""
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
@@ -466,6 +517,7 @@ def mxfp4_quantize(x: torch.Tensor, plain_scales: bool = True, mma_scales: bool 
     return Quantized(codes, scales, smma, torch.ones(1, dtype=torch.float32, device=dev), rows, cols)
 
 
+@_on_stream
 def mxfp4_gemm(a: Quantized, b: Quantized, out_dtype: int = NVFP4_OUT_BF16, stream=None) -> torch.Tensor:
     """C = A . B^T of two MXFP4 operands (K-major)."""
     M, K, N = a.rows, a.cols, b.rows
@@ -476,6 +528,7 @@ def mxfp4_gemm(a: Quantized, b: Quantized, out_dtype: int = NVFP4_OUT_BF16, stre
     return out
 
 
+@_on_stream
 def quantize_dual(x: torch.Tensor, rounding: int = NVFP4_RNE, sr_seed: int = 0, rht_seed: int = 0,
                   sr_seed_t: int = 0, stream=None):
     """(Q1, Q2): x row-wise and RHT(x^T), from one shared amax read."""
@@ -521,17 +574,9 @@ def _padded(rows: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
     return t if ld == cols else t.narrow(1, 0, cols)
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Device scratch of one call: not reused before that call's stream is past it."""
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    return _kept(ws, stream)
-
-
-def _kept(t: torch.Tensor, stream) -> torch.Tensor:
-    """t, allocated on the current stream and used on `stream`."""
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
-    return t
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """Device scratch of one call, allocated on the stream that it is used on."""
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
@@ -548,6 +593,7 @@ def _check_word(t):
         _here(t)
 
 
+@_on_stream
 def gemm_epilogue(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, M: int, N: int, K: int, bias=None,
                   activation: int = NVFP4_ACT_NONE, residual: Optional[torch.Tensor] = None,
                   out_dtype: int = NVFP4_OUT_BF16, out: Optional[torch.Tensor] = None,
@@ -586,6 +632,7 @@ def _gemm_layer(plan, a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, 
     return out
 
 
+@_on_stream
 def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_grad: bool = True,
              plan: "Optional[MoePlan]" = None, out: Optional[torch.Tensor] = None,
              amax_out: Optional[torch.Tensor] = None, stream=None):
@@ -605,7 +652,7 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], activation: int, bias_
     experts = 0 if plan is None else plan.experts
     if bias_grad:
         dbias = dy.new_empty((experts, N) if experts else (N,), dtype=torch.float32)
-        ws = _scratch(nvfp4_act_grad_workspace_size(M, N), dy.device, stream)
+        ws = _scratch(nvfp4_act_grad_workspace_size(M, N), dy.device)
     nvfp4_act_grad(dy, ldy, z, ldz, M, N, activation, plan.offsets if experts else None,
                    plan.counts if experts else None, experts, out, lddz, dbias, amax_out, ws,
                    ws.numel() if bias_grad else 0, stream)
@@ -630,6 +677,7 @@ class MoePlan:
         self.tokens, self.topk = self.copy_row.shape
 
 
+@_on_stream
 def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None, stream=None) -> MoePlan:
     """Sort the copies of int32 expert_ids [tokens x topk] by expert.  rows (default: enough for every routing)
     bounds the sorted matrices; copies that find no row are dropped."""
@@ -641,7 +689,7 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
     ws_bytes = nvfp4_moe_workspace_size(n, experts)
     # one allocation: the call's scratch, then the plan's four arrays
     sizes = (ws_bytes // 4, experts + 1, experts, rows, n)
-    buf = _kept(expert_ids.new_empty(sum(sizes)), stream)
+    buf = expert_ids.new_empty(sum(sizes))
     ws = buf.data_ptr()
     offsets = ws + ws_bytes
     counts = offsets + 4 * experts + 4
@@ -651,6 +699,7 @@ def moe_sort(expert_ids: torch.Tensor, experts: int, rows: Optional[int] = None,
     return MoePlan(offsets, counts, row_copy, copy_row.view(expert_ids.shape))
 
 
+@_on_stream
 def moe_gather(x: torch.Tensor, plan: MoePlan, out: Optional[torch.Tensor] = None,
                amax_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The token rows x bf16 [tokens x cols] sorted by expert: bf16 [rows x cols], zeros in padding rows.  With
@@ -671,6 +720,7 @@ def _check_weights(weights, plan):
         _here(weights)
 
 
+@_on_stream
 def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] = None,
                 residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
@@ -686,6 +736,7 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] 
     return out
 
 
+@_on_stream
 def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], plan: MoePlan,
                      weights: Optional[torch.Tensor] = None, amax_out: Optional[torch.Tensor] = None, stream=None):
     """(dy, dweights) of moe_combine: dy bf16 [rows x cols] with zeros in padding rows, dweights fp32
@@ -702,6 +753,7 @@ def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], plan: MoePla
     return dy, dw
 
 
+@_on_stream
 def gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan: MoePlan, M: int, N: int, K: int,
                  bias=None, activation: int = NVFP4_ACT_NONE, residual: Optional[torch.Tensor] = None,
                  out_dtype: int = NVFP4_OUT_BF16, out: Optional[torch.Tensor] = None,
@@ -717,6 +769,7 @@ def gemm_grouped(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan:
                        residual, out_dtype, out, pre, amax_out, stream)
 
 
+@_on_stream
 def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs, plan: MoePlan, M: int, N: int,
                        K: int, out_dtype: int = NVFP4_OUT_F32, out: Optional[torch.Tensor] = None,
                        stream=None) -> torch.Tensor:
@@ -737,6 +790,7 @@ def gemm_grouped_wgrad(a_codes, a_scales_mma, a_gs, b_codes, b_scales_mma, b_gs,
     return out
 
 
+@_on_stream
 def quantize_2d_experts(w: torch.Tensor, columnwise: bool = True, stream=None):
     """(W, W^T) operands of gemm_grouped from expert weights bf16 [experts x rows x cols], each quantized by
     quantize_2d: Quantized with stacked codes, scales and global scales (the second None without columnwise)."""
@@ -750,7 +804,7 @@ def quantize_2d_experts(w: torch.Tensor, columnwise: bool = True, stream=None):
     col = Quantized(torch.empty(experts, cols, rows // 2, dtype=torch.uint8, device=dev), None,
                     torch.empty(experts, nvfp4_mma_scale_bytes(cols, rows), dtype=torch.uint8, device=dev),
                     row.global_scale, cols, rows) if columnwise else None
-    ws = _scratch(nvfp4_workspace_size(rows, cols), dev, stream)
+    ws = _scratch(nvfp4_workspace_size(rows, cols), dev)
     for e in range(experts):
         nvfp4_quantize_2d(w[e], rows, cols, w.stride(1), row.codes[e], col.codes[e] if columnwise else None, None,
                           row.scales_mma[e], col.scales_mma[e] if columnwise else None, row.global_scale[e:e + 1],

@@ -208,7 +208,7 @@ def test_act_grad_refuses_a_plan_that_is_not_on_the_current_device(monkeypatch):
     monkeypatch.setattr(N, "_here", lambda *t: here(*(x for x in t if x.dtype is torch.int32)) if any(
         x.dtype is torch.int32 for x in t) else matrices.append(t))
     monkeypatch.setattr(N, "nvfp4_act_grad", lambda *a, **k: pytest.fail("launched with a plan elsewhere"))
-    monkeypatch.setattr(N, "_scratch", lambda n, device, stream: torch.empty(max(n, 16), dtype=torch.uint8))
+    monkeypatch.setattr(N, "_scratch", lambda n, *where: torch.empty(max(n, 16), dtype=torch.uint8))
     plan = N.MoePlan(*(torch.zeros(s, dtype=torch.int32) for s in (3, 2, 256, (8, 2))))
     dy = torch.zeros(256, 64, dtype=torch.bfloat16)
     with pytest.raises(AssertionError, match="current CUDA device"):
