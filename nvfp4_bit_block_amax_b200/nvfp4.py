@@ -408,7 +408,8 @@ _ws_cache = {}
 
 
 def workspace(device=None) -> torch.Tensor:
-    """A per-device scratch buffer for the amax partials (allocated by torch)."""
+    """A per-device scratch buffer for the amax partials (allocated by torch), for callers of the C names that use one
+    stream at a time; the helpers take scratch of their own in each call."""
     dev = torch.device(device if device is not None else "cuda")
     key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
     ws = _ws_cache.get(key)
@@ -417,6 +418,11 @@ def workspace(device=None) -> torch.Tensor:
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _ws_cache[key] = ws
     return ws
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """Device scratch of one call, allocated on the stream that it is used on."""
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def _empty_u8(n, device):
@@ -438,7 +444,7 @@ def quantize_1d(x: torch.Tensor, transpose: bool = False, rounding: int = NVFP4_
     scales = torch.empty(qr, qc // 16, dtype=torch.uint8, device=dev) if plain_scales else None
     smma = _empty_u8(nvfp4_mma_scale_bytes(qr, qc), dev) if mma_scales else None
     gs = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = workspace(dev)
+    ws = _scratch(nvfp4_workspace_size(rows, cols), dev) if amax is None else None
     if amax is not None:
         assert not rht, "the amax of the rotated tensor is not known to a producer"
         nvfp4_quantize_1d_from_amax(x, rows, cols, x.stride(0), int(transpose), rounding, sr_seed, amax, codes,
@@ -468,7 +474,7 @@ def quantize_2d(w: torch.Tensor, columnwise: bool = True, plain_scales: bool = T
     mr = _empty_u8(nvfp4_mma_scale_bytes(rows, cols), dev) if mma_scales else None
     mc = _empty_u8(nvfp4_mma_scale_bytes(cols, rows), dev) if (mma_scales and columnwise) else None
     gs = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = workspace(dev)
+    ws = _scratch(nvfp4_workspace_size(rows, cols), dev) if amax is None else None
     if amax is not None:
         nvfp4_quantize_2d_from_amax(w, rows, cols, w.stride(0), amax, cr, cc, sc, mr, mc, gs, stream)
     else:
@@ -572,11 +578,6 @@ def _padded(rows: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
     ld = (cols + 7) // 8 * 8
     t = like.new_empty((rows, ld), dtype=dtype)
     return t if ld == cols else t.narrow(1, 0, cols)
-
-
-def _scratch(nbytes: int, device) -> torch.Tensor:
-    """Device scratch of one call, allocated on the stream that it is used on."""
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):

@@ -122,6 +122,29 @@ def test_the_default_streams_handles(fake):
         fake["recorded"].clear()
 
 
+def test_scratch_is_not_shared_between_calls(fake, monkeypatch):
+    """Two calls on two streams, or two captured graphs, may run at once."""
+    monkeypatch.setattr(N, "workspace", lambda dev=None: pytest.fail("one workspace for every stream"))
+    for name in NAMES:
+        calls()[name][1](stream=None)
+
+
+@pytest.mark.gpu
+def test_quantizers_on_two_streams_at_once():
+    """Maxima that differ by call: with shared scratch one call's would show in the other's scale."""
+    xs = [torch.randn(4096, 2048, device="cuda").bfloat16() * 10.0 ** i for i in range(2)]
+    makes = (lambda x, s: N.quantize_1d(x, stream=s), lambda x, s: N.quantize_2d(x, stream=s))
+    want = [[m(x, None) for x in xs] for m in makes]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for m, ws in zip(makes, want):
+        for _ in range(20):
+            got = [m(x, s) for x, s in zip(xs, streams)]
+            torch.cuda.synchronize()
+            for g, w in zip(got, ws):
+                assert torch.equal(g.global_scale, w.global_scale) and torch.equal(g.codes, w.codes)
+
+
 @pytest.mark.gpu
 def test_dropped_results_are_not_handed_out_while_the_other_stream_writes_them():
     side = torch.cuda.Stream()
