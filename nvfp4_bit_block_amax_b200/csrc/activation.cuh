@@ -35,6 +35,14 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// max(x, 0) that leaves NaN as it is (fmaxf gives the other operand): a step
+// that has diverged shows in the layer's results.
+__device__ __forceinline__ float max0(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // exp(-x) overflows to infinity below x = -88, where the quotient is 0.
 __device__ __forceinline__ float logistic(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }
 
@@ -65,9 +73,9 @@ constexpr float kTanhCubic = 0.044715f;
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == ACT_RELU) return fmaxf(z, 0.0f);
+    if constexpr (ACT == ACT_RELU) return max0(z);
     if constexpr (ACT == ACT_RELU2) {
-        const float r = fmaxf(z, 0.0f);
+        const float r = max0(z);
         return r * r;
     }
     if constexpr (ACT == ACT_GELU) return z * normal(z).cdf;
@@ -78,7 +86,7 @@ __device__ __forceinline__ float act_value(float z) {
 
 template <int ACT>   // not for NONE and RELU2, see act_grad_value
 __device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;   // NaN's slope is NaN
     if constexpr (ACT == ACT_GELU) {
         const Normal n = normal(z);
         return n.pdf == 0.0f ? n.cdf : fmaf(z, n.pdf, n.cdf);   // 0 far out, where z may be anything
@@ -100,7 +108,7 @@ __device__ __forceinline__ float act_slope(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad_value(float g, float z) {
     if constexpr (ACT == ACT_NONE) return g;
-    else if constexpr (ACT == ACT_RELU2) return 2.0f * (g * fmaxf(z, 0.0f));
+    else if constexpr (ACT == ACT_RELU2) return 2.0f * (g * max0(z));
     else return g * act_slope<ACT>(z);
 }
 
