@@ -68,6 +68,12 @@ __device__ __forceinline__ Normal normal(float z) {
     return Normal{z > 0.0f ? 1.0f - tail : tail, 0.3989422804f * e};
 }
 
+// z P(z) = max(z, 0) - |z| P(-|z|); the product takes z no further than the
+// largest number, so that infinity less a tail of zero stays infinity.
+__device__ __forceinline__ float gelu_value(float z, float tail) {
+    return fmaf(-fabsf(fminf(z, 0x1.fffffep127f)), tail, fmaxf(z, 0.0f));
+}
+
 constexpr float kTanhScale2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
@@ -78,7 +84,10 @@ __device__ __forceinline__ float act_value(float z) {
         const float r = max0(z);
         return r * r;
     }
-    if constexpr (ACT == ACT_GELU) return z * normal(z).cdf;
+    if constexpr (ACT == ACT_GELU) {
+        const Normal n = normal(-fabsf(z));
+        return gelu_value(z, n.cdf);
+    }
     if constexpr (ACT == ACT_GELU_TANH) return z * logistic(kTanhScale2 * z * fmaf(kTanhCubic * z, z, 1.0f));
     if constexpr (ACT == ACT_SILU) return z * logistic(z);
     return z;
@@ -134,9 +143,8 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
         poly = __ffma2_rn(t, poly, both(0.5f * kHastings3));
         poly = __ffma2_rn(t, poly, both(0.5f * kHastings2));
         poly = __ffma2_rn(t, poly, both(0.5f * kHastings1));
-        // z P(z) = max(z, 0) - |z| P(-|z|)
         const float2 tail = __fmul2_rn(__fmul2_rn(t, poly), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
-        return make_float2(fmaf(-fabsf(z.x), tail.x, fmaxf(z.x, 0.0f)), fmaf(-fabsf(z.y), tail.y, fmaxf(z.y, 0.0f)));
+        return make_float2(gelu_value(z.x, tail.x), gelu_value(z.y, tail.y));
     } else return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
 }
 

@@ -50,3 +50,40 @@ def test_nan_stays_in_the_gradient(act, cols):
     ok()
     nan = (dy if zz is None else zz).isnan()
     assert torch.equal(dz.isnan(), nan) and torch.equal(db.isnan(), nan.any(0))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("Nn", [64, 131])
+@pytest.mark.parametrize("value,want", [(INF, INF), (3e38, None), (-INF, None)])
+def test_infinities_through_the_activations(act, M, Nn, value, want):
+    """act(inf) = inf for all of them; 3e38 stays itself (its square overflows); at -inf relu and relu2 are 0, and the
+    products z P(z), z s(z) with a factor of 0 are NaN, as their definitions are."""
+    bias = biases(Nn, value)
+    c = layer(M, Nn, bias, act)[:, ::5]
+    z = bias[::5].float()
+    if value == -INF:
+        zero = act in (N.NVFP4_ACT_RELU, N.NVFP4_ACT_RELU2)
+        assert (c == 0).all() if zero else (c == -INF).all() if act == N.NVFP4_ACT_NONE else c.isnan().all()
+    elif want or act == N.NVFP4_ACT_RELU2:
+        assert (c == INF).all()
+    else:                                            # z times a reciprocal that may be off by a step
+        assert ((c - z).abs() <= z * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_both_kernels_on_a_product_that_overflows(act):
+    """Finite operands whose z passes binary32: the few-row and the many-row kernel say the same."""
+    K, Nn = 128, 72
+    x = torch.ones(200, K, device="cuda").bfloat16()
+    w = torch.ones(Nn, K, device="cuda").bfloat16()
+    w[::3] *= -1
+    a, b = N.quantize_1d(x), N.quantize_1d(w)
+    big = torch.full((1,), 1e19, device="cuda")
+    run = lambda M: N.gemm_epilogue(a.codes[:M], a.scales_mma, big, b.codes, b.scales_mma, big, M, Nn, K,
+                                    activation=act, out_dtype=N.NVFP4_OUT_F32)
+    many, few = run(200), run(8)
+    ok()
+    z = torch.where(torch.arange(Nn, device="cuda") % 3 == 0, -INF, INF)
+    assert torch.equal(many[:8].nan_to_num(nan=5.0, posinf=INF, neginf=-INF), few.nan_to_num(nan=5.0, posinf=INF, neginf=-INF))
+    assert (many[:, z > 0] == INF).all()
