@@ -107,8 +107,8 @@ __device__ __forceinline__ float act_slope(float z) {
         return d == 0.0f ? s : fmaf(d, kTanhScale2 * z * fmaf(3.0f * kTanhCubic, zz, 1.0f), s);
     }
     if constexpr (ACT == ACT_SILU) {
-        const float s = logistic(z);
-        return fmaf(z, s * (1.0f - s), s);
+        const float s = logistic(z), d = s * (1.0f - s);   // 0 far out, where z may be infinite
+        return d == 0.0f ? s : fmaf(z, d, s);
     }
 }
 

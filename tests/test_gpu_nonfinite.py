@@ -87,3 +87,15 @@ def test_both_kernels_on_a_product_that_overflows(act):
     z = torch.where(torch.arange(Nn, device="cuda") % 3 == 0, -INF, INF)
     assert torch.equal(many[:8].nan_to_num(nan=5.0, posinf=INF, neginf=-INF), few.nan_to_num(nan=5.0, posinf=INF, neginf=-INF))
     assert (many[:, z > 0] == INF).all()
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_at_infinity_in_whole_and_ragged_columns(act):
+    """The slope's limits, 0 and 1 (relu2: 0 and inf), in every column: the last ones of a ragged row go one by one."""
+    z = torch.tensor([-INF, INF], device="cuda").repeat(40)[:19].repeat(3, 1)
+    pad = torch.zeros(3, 24, device="cuda").bfloat16()
+    pad[:, :19] = z.bfloat16()
+    dz, _ = N.act_grad(torch.ones_like(pad)[:, :19], pad[:, :19], act)
+    ok()
+    top = INF if act == N.NVFP4_ACT_RELU2 else 1.0
+    assert torch.equal(dz.float(), torch.where(z > 0, top, 0.0))
