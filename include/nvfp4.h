@@ -367,7 +367,8 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
  *              aligned.  It may be C itself (bf16 C, ldr == ldc).
  *   pre        bf16 [M x ldp], nullable: receives RN(z), what the gradient
  *              needs; ldp and alignment as residual.
- *   c_amax     as nvfp4_gemm_amax, nullable.
+ *   c_amax     max |C| over the stored values, nullable; NaN where C holds one
+ *              (so with every maximum of the calls below).
  *   All of it is binary32; z is rounded only where it is stored, C once.
  *   Columns from N on are left as they were, in C and in pre. */
 nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,

@@ -35,13 +35,14 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// max(x, 0) that leaves NaN as it is (fmaxf gives the other operand): a step
-// that has diverged shows in the layer's results.
-__device__ __forceinline__ float max0(float x) {
-    float y;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
-    return y;
+// Maxima that leave NaN as it is (fmaxf gives the other operand): a step that
+// has diverged shows in the layer's results.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
+__device__ __forceinline__ float max0(float x) { return max_nan(x, 0.0f); }
 
 // exp(-x) overflows to infinity below x = -88, where the quotient is 0.
 __device__ __forceinline__ float logistic(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }

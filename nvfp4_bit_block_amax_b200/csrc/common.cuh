@@ -47,6 +47,12 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t acc, uint32_t w) {
     asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(acc), "r"(w));
     return d;
 }
+// The same with NaN kept: a maximum over values that hold one is NaN.
+__device__ __forceinline__ uint32_t absmax2_nan(uint32_t acc, uint32_t w) {
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(acc), "r"(w));
+    return d;
+}
 __device__ __forceinline__ uint32_t absmax2_fold(uint32_t acc) {   // -> binary32 bits of the max
     const uint32_t lo = acc & 0x7FFFu, hi = (acc >> 16) & 0x7FFFu;
     return (lo > hi ? lo : hi) << 16;

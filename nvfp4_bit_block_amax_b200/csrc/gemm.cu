@@ -963,11 +963,11 @@ __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, in
                     uint32_t m = 0;
                     if (ni >= 32) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) m = absmax2(m, w[j]);
+                        for (int j = 0; j < 16; ++j) m = absmax2_nan(m, w[j]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            m = absmax2(m, 2 * j + 1 < ni ? w[j] : 2 * j < ni ? w[j] & 0xFFFFu : 0u);
+                            m = absmax2_nan(m, 2 * j + 1 < ni ? w[j] : 2 * j < ni ? w[j] & 0xFFFFu : 0u);
                     }
                     amax_acc = max(amax_acc, absmax2_fold(m));
                 }
@@ -978,8 +978,8 @@ __device__ __forceinline__ bool epilogue_ext(const KParams& p, const Tile& t, in
                     float peak = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        if (2 * j < ni) peak = fmaxf(peak, fabsf(v[j].x));
-                        if (2 * j + 1 < ni) peak = fmaxf(peak, fabsf(v[j].y));
+                        if (2 * j < ni) peak = max_nan(peak, fabsf(v[j].x));
+                        if (2 * j + 1 < ni) peak = max_nan(peak, fabsf(v[j].y));
                     }
                     amax_acc = max(amax_acc, __float_as_uint(peak));
                 }

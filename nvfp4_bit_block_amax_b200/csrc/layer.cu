@@ -49,11 +49,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 __device__ __forceinline__ uint32_t absmax8(uint32_t acc, const uint4& w) {
-    return absmax2(absmax2(absmax2(absmax2(acc, w.x), w.y), w.z), w.w);
+    return absmax2_nan(absmax2_nan(absmax2_nan(absmax2_nan(acc, w.x), w.y), w.z), w.w);
 }
 
 // Fold every thread's packed |bf16| maximum into *amax (binary32, zeroed by
 // the caller): one atomic per CTA, none where the word is already as large.
+// As bits a NaN is above every number, so it stays.
 __device__ __forceinline__ uint32_t cta_max(uint32_t m) {   // the result in thread 0
     __shared__ uint32_t s_max[kWarps];
     m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
                                                     ACT == ACT_NONE ? 0.0f : __bfloat162float(p.z[r * p.ldz + col + e]));
                         sum[e] += v;
                         const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                        peak = absmax2(peak, (uint32_t)__bfloat16_as_ushort(h));
+                        peak = absmax2_nan(peak, (uint32_t)__bfloat16_as_ushort(h));
                         p.dz[r * p.lddz + col + e] = h;
                     }
             }

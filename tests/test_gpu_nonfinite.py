@@ -43,7 +43,7 @@ def test_nan_stays(act, M, Nn, dtype):
 def test_nan_stays_in_the_gradient(act, cols):
     zz = bf16(200, (cols + 7) // 8 * 8, seed=2)[:, :cols]
     zz[::7, ::5] = NAN
-    dy = torch.ones_like(zz)
+    dy = torch.ones(200, (cols + 7) // 8 * 8, device="cuda").bfloat16()[:, :cols]     # rows on 16-byte boundaries
     if act == N.NVFP4_ACT_NONE:
         dy, zz = zz, None
     dz, db = N.act_grad(dy, zz, act)
@@ -99,3 +99,59 @@ def test_slopes_at_infinity_in_whole_and_ragged_columns(act):
     ok()
     top = INF if act == N.NVFP4_ACT_RELU2 else 1.0
     assert torch.equal(dz.float(), torch.where(z > 0, top, 0.0))
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("Nn,at", [(64, 0), (131, 129), (131, 130), (300, 255)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_products_maximum(M, Nn, at, dtype):
+    for value in (NAN, INF, -INF):
+        bias = torch.linspace(-3, 3, Nn, device="cuda").bfloat16()
+        bias[at] = value
+        amax = torch.zeros(1, device="cuda")
+        layer(M, Nn, bias, N.NVFP4_ACT_NONE, dtype, amax_out=amax)
+        assert amax.isnan().item() if value != value else amax.item() == INF
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 64), (130, 131), (4000, 256)])
+@pytest.mark.parametrize("bias_grad", [True, False])
+def test_the_gradients_maximum(rows, cols, bias_grad):
+    for value in (NAN, INF):
+        dy = bf16(rows, (cols + 7) // 8 * 8, seed=3)[:, :cols]
+        dy[rows - 1, cols - 1] = value
+        amax = torch.zeros(1, device="cuda")
+        N.act_grad(dy, None, N.NVFP4_ACT_NONE, bias_grad=bias_grad, amax_out=amax)
+        ok()
+        assert amax.isnan().item() if value != value else amax.item() == INF
+
+
+@pytest.mark.parametrize("tokens,cols", [(3, 64), (400, 1032), (3000, 64)])
+def test_the_movements_maxima(tokens, cols):
+    ids = (torch.arange(2 * tokens, device="cuda", dtype=torch.int32) * 5 % 4).reshape(tokens, 2).contiguous()
+    plan = N.moe_sort(ids, 4)
+    x = bf16(tokens, cols, seed=4)
+    x[tokens - 1, cols - 1] = NAN
+    first, second = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    N.moe_gather(x, plan, amax_out=first)
+    N.moe_combine_grad(x, None, plan, amax_out=second)
+    ok()
+    assert first.isnan().item() and second.isnan().item()
+
+
+@pytest.mark.parametrize("rows", [None, 4096])
+def test_the_experts_maximum(rows):
+    """By expert, few rows and many; the NaN of an expert without tokens counts nowhere."""
+    E, Nn, K = 4, 136, 128
+    ids = torch.tensor([[0, 1], [1, 3], [0, 3]], dtype=torch.int32, device="cuda")
+    plan = N.moe_sort(ids, E, rows=rows)
+    a = N.quantize_1d(N.moe_gather(bf16(3, K, seed=5), plan))
+    w = N.quantize_2d_experts(torch.zeros(E, 144, K, device="cuda").bfloat16(), columnwise=False)[0]
+    codes, scales = w.codes[:, :Nn].contiguous(), w.scales_mma
+    for expert, dtype in ((2, torch.float32), (3, torch.float32), (3, torch.bfloat16)):
+        bias = torch.ones(E, Nn, device="cuda").bfloat16()
+        bias[expert, Nn - 1] = NAN
+        amax = torch.zeros(1, device="cuda")
+        N.gemm_grouped(*quant_args(a), codes, scales, w.global_scale, plan, plan.rows, Nn, K, bias=bias, amax_out=amax,
+                       out_dtype=N.NVFP4_OUT_F32 if dtype == torch.float32 else N.NVFP4_OUT_BF16)
+        ok()
+        assert amax.item() == 1.0 if expert == 2 else amax.isnan().item()
