@@ -47,26 +47,45 @@ __device__ __forceinline__ float max0(float x) { return max_nan(x, 0.0f); }
 // exp(-x) overflows to infinity below x = -88, where the quotient is 0.
 __device__ __forceinline__ float logistic(float x) { return rcp_fast(1.0f + exp2_fast(-kLog2e * x)); }
 
-// The normal distribution function and its density, by Hastings' polynomial
-// for the error function (Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26): with x = |z| / sqrt(2) and t = 1 / (1 + 0.3275911 x),
-// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) to 1.5e-7, and the error falls off
-// with exp(-x^2) like the function, so that P(-|z|) = erfc(x) / 2 is good far
-// out too.  One exponential and one division serve both results; the library's
-// normcdff takes three times the instructions.
-constexpr float kHastingsP = 0.3275911f * 0.70710678f;   // of |z|, not of x
-constexpr float kHastings1 = 0.254829592f, kHastings2 = -0.284496736f, kHastings3 = 1.421413741f,
-                kHastings4 = -1.453152027f, kHastings5 = 1.061405429f;
+// The normal distribution function's tail, P(-x) = exp(-x^2 / 2) R(x) for x >= 0:
+// R falls smoothly from 1/2 to 1 / (x sqrt(2 pi)), so with t = 1 / (1 + p x) it is
+// close to a polynomial in t without a constant term.  The seven coefficients
+// are a minimax fit made for this file (p chosen with them) to the smaller of
+// two bounds, 1e-7 absolute in P and 5e-5 relative; it reaches 0.3 of both.  In
+// binary32 P(-x) is off by at most 1.7e-7, and relative to itself by 1.6e-5 plus
+// x^2 2^-23 from the rounded exponent, down to where it leaves the normal range
+// at x = 13: a hundredth of bf16's half step, so a stored gelu is right far
+// out too, where a fit with an absolute bound alone (five terms) was off by
+// 0.4 % at 6 and 1.5 % at 9.  One exponential and one reciprocal serve
+// function and density.
+constexpr float kTailP = 0.2609f;
+constexpr float kTail1 = 0.10401621460914612f, kTail2 = 0.10570815950632095f, kTail3 = 0.08265645802021027f,
+                kTail4 = 0.14435040950775146f, kTail5 = -0.07746347039937973f, kTail6 = 0.20951735973358154f,
+                kTail7 = -0.068785160779953f;
+// exp(-x^2 / 2) and R(x), x = |z|.
+struct Tail {
+    float2 e, r;
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Tail tail2(float2 z) {
+    const float2 q = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
+    const float2 d = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(kTailP), both(1.0f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    float2 r = __ffma2_rn(t, both(kTail7), both(kTail6));
+    r = __ffma2_rn(t, r, both(kTail5));
+    r = __ffma2_rn(t, r, both(kTail4));
+    r = __ffma2_rn(t, r, both(kTail3));
+    r = __ffma2_rn(t, r, both(kTail2));
+    r = __ffma2_rn(t, r, both(kTail1));
+    return Tail{make_float2(exp2_fast(q.x), exp2_fast(q.y)), __fmul2_rn(t, r)};
+}
 struct Normal {
     float cdf, pdf;
 };
 __device__ __forceinline__ Normal normal(float z) {
-    const float e = exp2_fast(-0.5f * kLog2e * z * z);
-    const float t = rcp_fast(fmaf(kHastingsP, fabsf(z), 1.0f));
-    const float poly =
-        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, kHastings5, kHastings4), kHastings3), kHastings2), kHastings1);
-    const float tail = 0.5f * poly * e;
-    return Normal{z > 0.0f ? 1.0f - tail : tail, 0.3989422804f * e};
+    const Tail w = tail2(both(z));
+    const float tail = w.e.x * w.r.x;
+    return Normal{z > 0.0f ? 1.0f - tail : tail, 0.3989422804f * w.e.x};
 }
 
 // z P(z) = max(z, 0) - |z| P(-|z|); the product takes z no further than the
@@ -124,7 +143,6 @@ __device__ __forceinline__ float act_grad_value(float g, float z) {
 
 // The activation of two values at once, through the two-wide multiply and add
 // where the formula is made of them.
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 logistic2(float2 x_log2e_neg) {   // of -x log2(e)
     const float2 d = __fadd2_rn(make_float2(exp2_fast(x_log2e_neg.x), exp2_fast(x_log2e_neg.y)), both(1.0f));
     return make_float2(rcp_fast(d.x), rcp_fast(d.y));
@@ -137,14 +155,8 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
         const float2 u = __ffma2_rn(zz, both(-kLog2e * kTanhScale2 * kTanhCubic), both(-kLog2e * kTanhScale2));
         return __fmul2_rn(z, logistic2(__fmul2_rn(z, u)));
     } else if constexpr (ACT == ACT_GELU) {
-        const float2 q = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
-        const float2 d = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(kHastingsP), both(1.0f));
-        const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
-        float2 poly = __ffma2_rn(t, both(0.5f * kHastings5), both(0.5f * kHastings4));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings3));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings2));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings1));
-        const float2 tail = __fmul2_rn(__fmul2_rn(t, poly), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
+        const Tail w = tail2(z);
+        const float2 tail = __fmul2_rn(w.r, w.e);
         return make_float2(gelu_value(z.x, tail.x), gelu_value(z.y, tail.y));
     } else return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
 }
@@ -164,15 +176,8 @@ __device__ __forceinline__ float2 act_grad_value2(float2 g, float2 z) {
         const float2 q = __fmul2_rn(z, dx);
         return __fmul2_rn(g, make_float2(d.x == 0.0f ? s.x : fmaf(d.x, q.x, s.x), d.y == 0.0f ? s.y : fmaf(d.y, q.y, s.y)));
     } else if constexpr (ACT == ACT_GELU) {
-        const float2 e = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
-        const float2 density = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-        const float2 t0 = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(kHastingsP), both(1.0f));
-        const float2 t = make_float2(rcp_fast(t0.x), rcp_fast(t0.y));
-        float2 poly = __ffma2_rn(t, both(0.5f * kHastings5), both(0.5f * kHastings4));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings3));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings2));
-        poly = __ffma2_rn(t, poly, both(0.5f * kHastings1));
-        const float2 tail = __fmul2_rn(__fmul2_rn(t, poly), density);
+        const Tail w = tail2(z);
+        const float2 density = w.e, tail = __fmul2_rn(w.r, density);
         const float2 cdf = make_float2(z.x > 0.0f ? 1.0f - tail.x : tail.x, z.y > 0.0f ? 1.0f - tail.y : tail.y);
         const float2 q = __fmul2_rn(z, both(0.3989422804f));
         return __fmul2_rn(g, make_float2(density.x == 0.0f ? cdf.x : fmaf(density.x, q.x, cdf.x),

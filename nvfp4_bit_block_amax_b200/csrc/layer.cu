@@ -81,6 +81,8 @@ __device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
 // up in order.  With 128 rows a thread goes through its rows in four steps of
 // four; where that leaves fewer than 4 CTAs to an SM, 32 rows give every
 // thread one step: 1000 x 4100 16.4 -> 12.3 us.
+// Four CTAs to an SM (64 registers): with gelu's 74, 16384 x 14336 takes 243 us
+// instead of 227.
 constexpr int kColTile = 256;
 constexpr int64_t kRowTile = 128, kRowTileFew = 32;
 
@@ -117,7 +119,7 @@ __device__ __forceinline__ int64_t live_rows(const int* offsets, const int* coun
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradParams p) {
+__global__ void __launch_bounds__(kThreads, 4) act_grad_kernel(ActGradParams p) {
     __shared__ float s_sum[kWarps][kColTile];
     wait_for_stream();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
