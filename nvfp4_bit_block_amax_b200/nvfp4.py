@@ -583,7 +583,7 @@ def _padded(rows: int, cols: int, dtype, like: torch.Tensor) -> torch.Tensor:
 def _check_operand(codes, scales_mma, gs, rows: int, k: int, experts: int = 1):
     assert codes.dtype is torch.uint8 and codes.numel() == experts * rows * (k // 2) and codes.is_contiguous()
     need = (rows + 127) // 128 * ((k // 16 + 3) // 4) * 512      # nvfp4_mma_scale_bytes
-    assert scales_mma.numel() >= experts * need and scales_mma.is_contiguous()
+    assert scales_mma.element_size() == 1 and scales_mma.numel() >= experts * need and scales_mma.is_contiguous()
     assert gs.dtype is torch.float32 and gs.numel() == experts and gs.is_contiguous()
     _here(codes, scales_mma, gs)
 

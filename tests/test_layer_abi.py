@@ -213,3 +213,17 @@ def test_act_grad_refuses_a_plan_that_is_not_on_the_current_device(monkeypatch):
     dy = torch.zeros(256, 64, dtype=torch.bfloat16)
     with pytest.raises(AssertionError, match="current CUDA device"):
         N.act_grad(dy, dy, N.NVFP4_ACT_SILU, plan=plan)
+
+
+def test_operands_scales_are_bytes(monkeypatch):
+    """A scale to an element: a wider type of as many elements is another array."""
+    monkeypatch.setattr(N, "_here", lambda *t: None)
+    monkeypatch.setattr(N, "nvfp4_gemm_epilogue", lambda *a, **k: None)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    op = lambda t: (u8(128, 32), torch.zeros(512, dtype=t), torch.zeros(1))
+    for wide in (torch.int32, torch.float32, torch.int16):
+        for a, b in ((wide, torch.uint8), (torch.uint8, wide)):
+            with pytest.raises(AssertionError):
+                N.gemm_epilogue(*op(a), *op(b), 128, 128, 64)
+    for byte in (torch.uint8, torch.float8_e4m3fn):
+        N.gemm_epilogue(*op(byte), *op(byte), 128, 128, 64)
