@@ -457,7 +457,11 @@ nvfp4_status nvfp4_moe_combine_grad(const void* dout, int64_t ldo, const void* y
  * nvfp4_mma_scale_bytes(N, K) bytes, b_gs [experts]; bias [experts x N].
  * Padding rows of C and pre become zeros (the residual is not added there),
  * whatever A holds in them.  With the codes of the transposed weights this is
- * the gradient with respect to A. */
+ * the gradient with respect to A.
+ *   M up to 159 experts + 127, which nvfp4_moe_rows gives for a mean of up to
+ *   32 copies per expert, goes to the kernel for few rows.  A smaller capacity
+ *   for segments known to be fuller than that is right too, but slower: give
+ *   rows beyond that limit then. */
 nvfp4_status nvfp4_gemm_grouped(const uint8_t* a_codes, const uint8_t* a_scales_mma, const float* a_gs,
                                 const uint8_t* b_codes, const uint8_t* b_scales_mma, const float* b_gs,
                                 const int32_t* offsets, const int32_t* counts, int64_t experts, int64_t M, int64_t N,

@@ -376,12 +376,21 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales_mm
 //   M x 4096 x 14336     64: 14.0 / 31.1                     128: 18.4 / 31.4   192: 28 / 31
 //   M x 1024 x 1024      64:  7.5 /  9.4   96:  9.9 /  9.5   128: 10.9 /  9.7   192: 17 / 10
 // so up to 128 rows.  How many rows each expert has is not known here, but segments are padded to 128: with
-// nvfp4_moe_rows, M / experts is about 127 more than the mean.  Mean 16, 32, 40 rows, the same two times:
-//   8 experts of 14336 x 4096    57 / 73   72 / 74   84 / 74
-//   64 experts of 2048 x 2048    36 / 57   45 / 55   49 / 55
-//   64 experts of 4096 x 1024    41 / 96   47 / 96   50 / 97
-//   16 experts of 4096 x 4096    34 / 46   45 / 47   47 / 47
-// so up to a mean of 32, which is one pass of that kernel.
+// nvfp4_moe_rows, M / experts is about 127 more than the mean.  Weights with tiles for every CTA, passes of 32 rows;
+// mean 16, 32, 40 rows, the same two times:
+//   8 experts of 14336 x 4096    58 / 70   59 / 70   97 / 70
+//   64 experts of 2048 x 2048    35 / 47   37 / 47   67 / 47
+//   64 experts of 4096 x 1024    40 / 65   44 / 66   74 / 66
+//   16 experts of 4096 x 4096    33 / 44   35 / 44   56 / 44
+// so up to a mean of 32, one pass.  Few and small weights, K split over a cluster, passes of 128; mean 32, 64, 128:
+//   1 expert of 14336 x 4096     14 / 17   16 / 18   18 / 18
+//   1 expert of 4096 x 1024       8 / 10    9 / 10   11 / 10
+//   3 experts of 2048 x 2048      8 / 11    9 / 11   13 / 11
+//   8 experts of 1024 x 4096     11 / 15   12 / 15   15 / 15
+// so where the rounding of M hides the mean (one expert's 2 to 129 rows are all M = 256), little is lost.
+// What M cannot tell: 128 rows an expert are the capacity of up to one copy each (64 experts of 2048 x 2048: 34 / 46),
+// but also a caller's own for segments that he knows to be full (97 / 46).  The first is every small batch; the second
+// can ask for the large product by a capacity beyond this limit (see nvfp4.h).
 static bool few_rows(const GemmExtArgs& g) { return g.experts ? g.M <= (127 + 32) * g.experts + 127 : g.M <= 128; }
 
 static nvfp4_status gemm_ext(GemmExtArgs g, int out_dtype, void* stream) {

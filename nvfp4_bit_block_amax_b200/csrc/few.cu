@@ -15,6 +15,11 @@
 //     in flight, several times what hides the latency of HBM.
 //   - Weights with more tiles than the GPU has SMs need no split: then a CTA
 //     streams through tiles (gemm_few_stream_kernel).
+//   - Experts with more rows than a pass takes (32 streaming, 128 in a cluster,
+//     where the few tiles leave more to gain: 2048 x 2048 with 128 rows 19 -> 10
+//     us): the passes behind the first are dealt to all CTAs or clusters, so
+//     that an expert which got most of the tokens does not leave the GPU to a
+//     few of them (2048 rows at one of 64 experts of 256 x 2048: 340 -> 15 us).
 // Measured in a chain (us, share of HBM's rate on the weight's bytes): one token
 // through 14336 x 4096 9.8 (0.51), 28672 x 8192 24.4 (0.83), 131072 x 4096 50
 // (0.91); 16 tokens x 2 through 8 experts of 14336 x 4096 56 (0.72).
@@ -47,6 +52,7 @@ constexpr int F_W_STAGE = F_ROWS * F_BKB;       // 16 KB
 constexpr int F_SF_STAGE = 4 * 512;             // 4 K steps of 128 rows x 4 scales
 constexpr int F_THREADS = 192;
 constexpr uint32_t F_TMEM = 256;
+constexpr int F_GROUPS = 5;                     // 32 experts each: more than 160 experts are never split
 
 // TOK: most tokens of one pass.
 template <int TOK>
@@ -277,9 +283,8 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), splits = (int)cluster_size();
-    const int unit = blockIdx.x / splits;
-    const int e = unit / p.tiles, tile = unit - e * p.tiles;
-    const int n0 = tile * F_ROWS;
+    const int unit = blockIdx.x / splits, units = gridDim.x / splits;
+    const int own = unit / p.tiles, own_tile = unit - own * p.tiles;
     const int steps = p.K / 64, blocks = (steps + 3) / 4;
     const int kb0 = (int)((int64_t)blocks * rank / splits), kb1 = (int)((int64_t)blocks * (rank + 1) / splits);
 
@@ -304,21 +309,38 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     wait_for_stream();
-    const int start = p.offsets ? segment_start(p.offsets, e, p.M) : 0;
-    const int stop = p.offsets ? segment_end(p.offsets, p.counts, e, p.M) : p.M;
+    const int own_start = p.offsets ? segment_start(p.offsets, own, p.M) : 0;
+    const int own_stop = p.offsets ? segment_end(p.offsets, p.counts, own, p.M) : p.M;
+    int rows[F_GROUPS];             // of experts 32 g + lane: under way during the first pass, looked at behind it
+#pragma unroll
+    for (int g = 0; g < F_GROUPS; ++g) rows[g] = p.offsets && 32 * g + lane < p.experts ? p.counts[32 * g + lane] : 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (L::kOwnSums && splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA runs
     const uint32_t tmem = *tmem_slot;
 
-    const Finish f = finish_at(p, e, n0 + 4 * lane);
     uint32_t amax = 0;
     int s = 0;                      // stage and its phase, of each role
     uint32_t phase = 0, acc_phase = 0;
     uint32_t issued_any = 0, issued_parity = 0;   // producer: the last phase issued on each stage
-    bool ok = true, freed = false;
-    for (int t0 = start; t0 < stop; t0 += TOK) {      // a pass over the weight for up to TOK tokens
+    bool ok = true, freed = false, first = true;
+    auto any_many = [&] {           // whether any expert has rows for a second pass
+        int most = rows[0];
+#pragma unroll
+        for (int g = 1; g < F_GROUPS; ++g) most = max(most, rows[g]);
+        return __any_sync(0xFFFFFFFFu, most > TOK) != 0;
+    };
+    // A pass over a weight tile for up to TOK tokens.  The CTAs of a cluster take the same passes, also after an abort.
+    auto pass = [&](int e, int tile, int t0, int stop) {
+        const Finish f = finish_at(p, e, (int64_t)tile * F_ROWS + 4 * lane);
+        if (!first) {               // the pass before is done with the accumulator and the stages
+            tc_fence_before();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (splits == 1) __syncthreads();
+            else cluster_sync();
+            tc_fence_after();
+        }
         const int tokens = min(TOK, stop - t0), boxes = (tokens + 15) / 16;
         if (warp == 0) {
             if (lane == 0) {
@@ -364,7 +386,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         while ((splits << shift) < tokens) ++shift;
         if (splits > 1) {
             // Every CTA of the cluster runs, and its stages (or, with sums of their own, those of the pass before) are free.
-            if (L::kOwnSums && t0 == start) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if (L::kOwnSums && first) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             else cluster_sync();
         }
         if (warp >= 2) {
@@ -387,14 +409,14 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         tc_fence_before();
         if (splits > 1) cluster_sync();
         else __syncthreads();
-        if (warp == 1 && t0 + TOK >= stop && !*abort_flag) {   // the last pass: nothing needs tensor memory any more
+        if (warp == 1 && !any_many() && !*abort_flag) {   // the only pass: nothing needs tensor memory any more
             freed = true;
             tc_fence_after();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM));
         }
         {
             const float4* part = reinterpret_cast<const float4*>(smem + L::kOffSums) + lane;
-            const int first = rank << shift, count = min(1 << shift, tokens - first);
+            const int from = rank << shift, count = min(1 << shift, tokens - from);
             for (int t = warp; t < count; t += F_THREADS / 32) {
                 float4 sum = part[t * (F_ROWS / 4)];
                 for (int c = 1; c < splits; ++c) {
@@ -404,15 +426,25 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                     sum.z += q.z;
                     sum.w += q.w;
                 }
-                finish<ACT>(p, f, t0 + first + t, sum, amax);
+                finish<ACT>(p, f, t0 + from + t, sum, amax);
             }
         }
-        if (t0 + TOK < stop) {      // the next pass writes the accumulator and the stages again
-            tc_fence_before();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (splits == 1) __syncthreads();
-            else cluster_sync();
-            tc_fence_after();
+        first = false;
+    };
+    if (own_start < own_stop) pass(own, own_tile, own_start, own_stop);
+    // Experts with more rows than one pass takes: their other passes, dealt to all clusters.
+    int next = 0;                   // the cluster whose turn it is
+#pragma unroll 1
+    for (int base = 0; base < (any_many() ? p.experts : 0); base += 32) {
+        unsigned more = __ballot_sync(0xFFFFFFFFu, base + lane < p.experts && p.counts[base + lane] > TOK);
+        while (more) {
+            const int e = base + __ffs(more) - 1;
+            more &= more - 1;
+            const int start = segment_start(p.offsets, e, p.M), stop = segment_end(p.offsets, p.counts, e, p.M);
+            const int64_t count = (int64_t)max((stop - start + TOK - 1) / TOK - 1, 0) * p.tiles;
+            for (int64_t i = (unit - next + units) % units; i < count; i += units)
+                pass(e, (int)(i % p.tiles), start + (int)(i / p.tiles + 1) * TOK, stop);
+            next = (int)((next + count) % units);
         }
     }
     if (p.c_amax) {                 // over the CTA, then one atomic
@@ -421,7 +453,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         if (lane == 0 && m) atomicMax(s_amax, m);
     }
     if (p.offsets && warp >= 2) {
-        zero_padding(p, e, n0, stop, rank * 4 + warp - 2, splits * 4, lane);
+        zero_padding(p, own, own_tile * F_ROWS, own_stop, rank * 4 + warp - 2, splits * 4, lane);
         zero_tail(p, blockIdx.x * 4 + warp - 2, gridDim.x * 4, lane);
     }
     // After an abort, no copy and no MMA may be in flight when memory is released; otherwise every copy was waited for by
@@ -738,8 +770,8 @@ cudaError_t launch_gemm_few(const GemmExtArgs& g, cudaStream_t s) {
     // The largest cluster whose CTAs are resident together (two to an SM) and have two blocks of K each.
     const int64_t units = (int64_t)p.tiles * p.experts, blocks = ceil_div(g.K, 256);
     int splits = 1;
-    while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits) splits *= 2;
-    const int tokens = g.offsets ? 32 : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
+    while (splits < 8 && units * splits * 2 <= 2 * sms && blocks >= 4 * splits && p.experts <= 32 * F_GROUPS) splits *= 2;
+    const int tokens = g.offsets ? (splits > 1 ? 128 : 32) : g.M <= 16 ? 16 : g.M <= 32 ? 32 : 128;
     if (splits == 1 && tokens <= 32) {
         const int grid = (int)(units < 2 * sms ? units : 2 * sms);
         return tokens == 16 ? launch_early(stream_kernel<16>(g.act), grid, S_THREADS, StreamLayout<16>::kBytes, s, 1, mw, mx, p)
