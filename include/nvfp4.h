@@ -85,7 +85,10 @@ enum {
 };
 
 /* Library ABI version (major * 100 + minor): 101 = 1.1, the 1.0 entry points
- * plus the dual, from-amax, GEMM-amax, MXFP4 and RHT-order ones. */
+ * plus the dual, from-amax, GEMM-amax, MXFP4 and RHT-order ones.  The linear
+ * layer's and the expert layer's entry points came later under the same
+ * number: a program that has to run with a library from before them looks one
+ * up by name (dlsym). */
 int nvfp4_version(void);
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -405,6 +408,7 @@ nvfp4_status nvfp4_act_grad(const void* dy, int64_t ldy, const void* z, int64_t 
  * the last segment, are padding: every call below writes zeros there.
  *
  * nvfp4_moe_sort: stable sort of `copies` = tokens x topk expert numbers.
+ *   copies     from 1; a step without tokens makes none of these calls.
  *   expert_ids int32 [copies], copy c = token c / topk; a number outside
  *              [0, experts) drops the copy.
  *   rows       rows of the sorted matrices, a multiple of 128.

@@ -77,7 +77,7 @@ __device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
 // 256 columns, and since segments start at multiples of 128 no tile crosses
 // one; a warp takes every 8th of the rows, a lane 8 columns.  6 bytes per
 // element moved; the sums of a tile's rows go to the workspace, [row tiles x N]
-// binary32 (1/64 of the bytes with 128 rows), and bias_grad_kernel adds them
+// binary32 (1/192 of the bytes with 128 rows, 1/48 with 32), and bias_grad_kernel adds them
 // up in order.  With 128 rows a thread goes through its rows in four steps of
 // four; where that leaves fewer than 4 CTAs to an SM, 32 rows give every
 // thread one step: 1000 x 4100 16.4 -> 12.3 us.
@@ -711,7 +711,7 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t s, int* launches) {
     p.copy_row = a.copy_row;
     p.chunk = (int)(ceil_div(ceil_div(a.n, sort_ctas(a.n, a.experts)), kThreads) * kThreads);
     const int ctas = (int)ceil_div(a.n, p.chunk);
-    const int smem = (int)(((kWarps + 2) * a.experts + 1) * 4);   // at most 41 KB: 1024 experts
+    const int smem = (int)(((kWarps + 2) * a.experts + 1) * 4);   // at most 20 KB: 512 experts
     if (ctas > 1) {
         *launches += 1;
         cudaError_t e = launch_early(sort_count_kernel, ctas, kThreads, p.experts * 4, s, 1, p);
