@@ -155,3 +155,19 @@ def test_the_experts_maximum(rows):
                        out_dtype=N.NVFP4_OUT_F32 if dtype == torch.float32 else N.NVFP4_OUT_BF16)
         ok()
         assert amax.item() == 1.0 if expert == 2 else amax.isnan().item()
+
+
+@pytest.mark.parametrize("M", [16, 272])
+def test_a_diverged_layer_shows_in_the_next_one(M):
+    """One NaN pre-activation: the maximum is NaN, so the quantizer's scale and all of the next product are."""
+    K = 256
+    x, w = N.quantize_1d(bf16(M, K, seed=6)), N.quantize_1d(bf16(K, K, seed=7, scale=K ** -0.5))
+    bias, amax = torch.zeros(K, device="cuda").bfloat16(), torch.zeros(1, device="cuda")
+    for value in (0.0, NAN):
+        bias[K - 1] = value
+        h = N.gemm_epilogue(*quant_args(x), *quant_args(w), M, K, K, bias=bias, activation=N.NVFP4_ACT_RELU,
+                            amax_out=amax)
+        q = N.quantize_1d(h, amax=amax)
+        y = N.gemm_epilogue(*quant_args(q), *quant_args(w), M, K, K)
+        ok()
+        assert y.isnan().all() if value != value else y.isfinite().all()

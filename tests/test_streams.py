@@ -188,3 +188,34 @@ def test_temporaries_on_another_stream():
         del junk
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.gpu
+def test_captured_on_a_forked_stream_and_on_the_default_streams_handle():
+    plan_ids = (torch.arange(120, device="cuda", dtype=I32) * 7 % 4).reshape(60, 2).contiguous()
+    x, side = torch.randn(60, 128, device="cuda").bfloat16(), torch.cuda.Stream()
+
+    def step(s):
+        plan = N.moe_sort(plan_ids, 4, stream=s)
+        return N.moe_combine(N.moe_gather(x, plan, stream=s), plan, stream=s)
+
+    want = step(None)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):                                        # two graphs, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            side.wait_stream(torch.cuda.current_stream())
+            out = step(side)
+            torch.cuda.current_stream().wait_stream(side)
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, out in graphs:
+            out.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for _, out in graphs)
+    with torch.cuda.stream(side):
+        got = [step(handle) for handle in (0, 1)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
