@@ -20,9 +20,10 @@
 //     us): the passes behind the first are dealt to all CTAs or clusters, so
 //     that an expert which got most of the tokens does not leave the GPU to a
 //     few of them (2048 rows at one of 64 experts of 256 x 2048: 340 -> 15 us).
-// Measured in a chain (us, share of HBM's rate on the weight's bytes): one token
-// through 14336 x 4096 9.8 (0.51), 28672 x 8192 24.4 (0.83), 131072 x 4096 50
-// (0.91); 16 tokens x 2 through 8 experts of 14336 x 4096 56 (0.72).
+// Measured in a captured graph, 400 MB of weights in turn (us, share of HBM's
+// rate on the weight's bytes): one token through 14336 x 4096 9.5 (0.53), 28672
+// x 8192 24.5 (0.82), 131072 x 4096 51.5 (0.89); 16 tokens x 2 through 8 experts
+// of 14336 x 4096 57 (0.71).
 //   - Warp 0: TMA producer.  Warp 1: the MMAs.  Warps 2 .. 5: block scales to
 //     tensor memory (a copy by the tensor core, tcgen05.cp, costs its pipe 64
 //     cycles; with 8 of them a block of K = 256 took 1015 cycles instead of

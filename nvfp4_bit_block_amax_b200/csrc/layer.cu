@@ -77,8 +77,8 @@ __device__ __forceinline__ void publish_amax(float* amax, uint32_t acc) {
 // 256 columns, and since segments start at multiples of 128 no tile crosses
 // one; a warp takes every 8th of the rows, a lane 8 columns.  6 bytes per
 // element moved; the sums of a tile's rows go to the workspace, [row tiles x N]
-// binary32 (1/192 of the bytes with 128 rows, 1/48 with 32), and bias_grad_kernel adds them
-// up in order.  With 128 rows a thread goes through its rows in four steps of
+// binary32 (1/192 of the bytes with 128 rows, 1/48 with 32), and
+// bias_grad_kernel adds them up in order.  With 128 rows a thread goes through its rows in four steps of
 // four; where that leaves fewer than 4 CTAs to an SM, 32 rows give every
 // thread one step: 1000 x 4100 16.4 -> 12.3 us.
 // Four CTAs to an SM (64 registers): with gelu's 74, 16384 x 14336 takes 243 us
